@@ -11,7 +11,7 @@ __all__ = ["synth"]
 
 
 def __getattr__(name):
-    if name.startswith("bitnet_") or name in ("BitnetError", "load_library"):
+    if name.startswith("bitnet_") or name in ("BitnetError", "KvCache", "load_library"):
         import importlib
         return getattr(importlib.import_module(".binding", __name__), name)
     raise AttributeError(name)

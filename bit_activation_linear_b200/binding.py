@@ -36,6 +36,20 @@ class BitnetError(RuntimeError):
         super().__init__(f"{where}: {text} ({status}): {detail}")
 
 
+class _CKvCache(ctypes.Structure):  # bitnet_kv_cache
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int64), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("page_tokens", ctypes.c_int32),
+                ("scale_tokens", ctypes.c_int32)]
+
+
+class _CKvBatch(ctypes.Structure):  # bitnet_kv_batch
+    _fields_ = [("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p), ("batch", ctypes.c_int64),
+                ("max_pages", ctypes.c_int64), ("tokens", ctypes.c_int64)]
+
+
 _SIGS = {
     "bitnet_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "bitnet_last_error": (ctypes.c_char_p, []),
@@ -131,6 +145,35 @@ _SIGS = {
     "bitnet_quant_states": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64,
                                            ctypes.c_int64, ctypes.c_int, ctypes.c_void_p,
                                            ctypes.c_void_p, ctypes.c_void_p]),
+    "bitnet_act_quant_residual_norm": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p,
+                                                      ctypes.c_int64, ctypes.c_int64,
+                                                      ctypes.c_void_p, ctypes.c_float,
+                                                      ctypes.c_int, ctypes.c_void_p,
+                                                      ctypes.c_void_p, ctypes.c_void_p,
+                                                      ctypes.c_void_p, ctypes.c_void_p]),
+    "bitnet_residual_norm_bitlinear_forward": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p,
+                                                              ctypes.c_int64, ctypes.c_int64,
+                                                              ctypes.c_void_p, ctypes.c_float,
+                                                              ctypes.c_void_p, ctypes.c_void_p,
+                                                              ctypes.c_int64, ctypes.c_int,
+                                                              ctypes.c_void_p, ctypes.c_void_p,
+                                                              ctypes.c_void_p, ctypes.c_size_t,
+                                                              ctypes.c_void_p]),
+    "bitnet_kv_cache_append": (ctypes.c_int, [ctypes.POINTER(_CKvCache),
+                                              ctypes.POINTER(_CKvBatch), ctypes.c_void_p,
+                                              ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
+                                              ctypes.c_void_p]),
+    "bitnet_kv_cache_read": (ctypes.c_int, [ctypes.POINTER(_CKvCache), ctypes.POINTER(_CKvBatch),
+                                            ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
+                                            ctypes.c_int64, ctypes.c_void_p]),
+    "bitnet_kv_attention_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(_CKvCache),
+                                                              ctypes.POINTER(_CKvBatch),
+                                                              ctypes.c_int64, ctypes.c_int64]),
+    "bitnet_kv_attention": (ctypes.c_int, [ctypes.POINTER(_CKvCache), ctypes.POINTER(_CKvBatch),
+                                           ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64,
+                                           ctypes.c_int64, ctypes.c_float, ctypes.c_int,
+                                           ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
+                                           ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
     "bitnet_sync_status": (ctypes.c_int, [ctypes.c_void_p]),
     "bitnet_selftest_wait_timeout": (ctypes.c_int, [ctypes.c_int64, ctypes.c_void_p]),
 }
@@ -641,6 +684,279 @@ def bitnet_quant_states(X: torch.Tensor, group: int, bits: int = 3, codes=None, 
     _rc(L.bitnet_quant_states(X.data_ptr(), M, C, int(group), int(bits), codes.data_ptr(),
                               scales.data_ptr(), _stream(stream)), "bitnet_quant_states")
     return codes, scales
+
+
+def _same_device(*tensors):
+    """The one device of these CUDA tensors, which has to be the current one: the library launches
+    on the current device."""
+    index = tensors[0].get_device()
+    for t in tensors:
+        if t.get_device() != index:
+            raise ValueError("all tensors must be on one device")
+    if index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on cuda:{index}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+
+
+def _empty(shape, dtype, device, stream):
+    """torch.empty in the pool of the stream that the call launches on, so that memory which is
+    freed right after the call is not handed to another stream while the kernels still use it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        stream = torch.cuda.ExternalStream(raw, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def bitnet_act_quant_residual_norm(X: torch.Tensor, R: torch.Tensor, norm_gain, eps: float,
+                                   act_bits: int, H=None, codes=None, scales=None, rowsum=None,
+                                   stream=None):
+    """Residual addition, RMS normalisation and per-token quantisation in one pass: H = X + R
+    (bf16; may be X or R), codes of the normalised H.  Returns (H, codes, scales, rowsum)."""
+    L = load_library()
+    _check(X, "X", torch.bfloat16, 2)
+    _check(R, "R", torch.bfloat16, 2)
+    M, K = X.shape
+    if R.shape != X.shape:
+        raise ValueError(f"R is {tuple(R.shape)}, X is {tuple(X.shape)}")
+    if H is None:
+        H = _empty((M, K), torch.bfloat16, X.device, stream)
+    else:
+        _check(H, "H", torch.bfloat16)
+        _nbytes_at_least(H, 2 * M * K, "H")
+    if codes is None:
+        codes = _empty((M, K if act_bits == 8 else K // 2),
+                       torch.int8 if act_bits == 8 else torch.uint8, X.device, stream)
+    else:
+        _check(codes, "codes")
+        _nbytes_at_least(codes, int(L.bitnet_act_codes_bytes(M, K, act_bits)), "codes")
+    if scales is None:
+        scales = _empty(M, torch.float32, X.device, stream)
+    else:
+        _check(scales, "scales", torch.float32)
+        _nbytes_at_least(scales, 4 * M, "scales")
+    if rowsum is None:
+        rowsum = _empty(M, torch.int32, X.device, stream)
+    else:
+        _check(rowsum, "rowsum", torch.int32)
+        _nbytes_at_least(rowsum, 4 * M, "rowsum")
+    gain = _gain_ptr(norm_gain, K)
+    _same_device(X, R, H, codes, scales, rowsum, *(() if norm_gain is None else (norm_gain,)))
+    _rc(L.bitnet_act_quant_residual_norm(X.data_ptr(), R.data_ptr(), M, K, gain, float(eps),
+                                         int(act_bits), H.data_ptr(), codes.data_ptr(),
+                                         scales.data_ptr(), rowsum.data_ptr(), _stream(stream)),
+        "bitnet_act_quant_residual_norm")
+    return H, codes, scales, rowsum
+
+
+def bitnet_residual_norm_bitlinear_forward(X, R, norm_gain, eps, Wp, gamma, act_bits=8, H=None,
+                                           Y=None, ws=None, stream=None):
+    """H = X + R (bf16; may be X or R), Y = BitLinear(RMSNorm(H)).  Returns (H, Y)."""
+    L = load_library()
+    _check(X, "X", torch.bfloat16, 2)
+    _check(R, "R", torch.bfloat16, 2)
+    _check(Wp, "Wp")
+    _check(gamma, "gamma", torch.float32)
+    M, K = X.shape
+    N = Wp.shape[0]
+    if R.shape != X.shape:
+        raise ValueError(f"R is {tuple(R.shape)}, X is {tuple(X.shape)}")
+    _nbytes_at_least(Wp, int(L.bitnet_packed_weight_bytes(N, K)), "Wp")
+    if H is None:
+        H = _empty((M, K), torch.bfloat16, X.device, stream)
+    else:
+        _check(H, "H", torch.bfloat16)
+        _nbytes_at_least(H, 2 * M * K, "H")
+    if Y is None:
+        Y = _empty((M, N), torch.bfloat16, X.device, stream)
+    else:
+        _check(Y, "Y", torch.bfloat16)
+        _nbytes_at_least(Y, 2 * M * N, "Y")
+    need = int(L.bitnet_workspace_bytes(M, K, N, act_bits))
+    if ws is None:
+        ws = _empty(max(need, 256), torch.uint8, X.device, stream)
+    else:
+        _check(ws, "ws")
+    gain = _gain_ptr(norm_gain, K)
+    _same_device(X, R, Wp, gamma, H, Y, ws, *(() if norm_gain is None else (norm_gain,)))
+    _rc(L.bitnet_residual_norm_bitlinear_forward(
+        X.data_ptr(), R.data_ptr(), M, K, gain, float(eps), Wp.data_ptr(), gamma.data_ptr(), N,
+        int(act_bits), H.data_ptr(), Y.data_ptr(), ws.data_ptr(),
+        ws.numel() * ws.element_size(), _stream(stream)),
+        "bitnet_residual_norm_bitlinear_forward")
+    return H, Y
+
+
+class KvCache:
+    """A paged 8-bit K/V cache (bitnet_kv_cache) over the caller's tensors: k_codes, v_codes int8
+    [num_pages, kv_heads, page_tokens, head_dim]; k_scales, v_scales float
+    [num_pages, kv_heads, page_tokens / scale_tokens].  It only holds and describes them."""
+
+    __slots__ = ("k_codes", "v_codes", "k_scales", "v_scales", "num_pages", "kv_heads",
+                 "page_tokens", "head_dim", "scale_tokens", "_c", "_ref")
+
+    def __init__(self, k_codes, v_codes, k_scales, v_scales):
+        for t, n in ((k_codes, "k_codes"), (v_codes, "v_codes")):
+            _check(t, n, torch.int8, 4)
+        for t, n in ((k_scales, "k_scales"), (v_scales, "v_scales")):
+            _check(t, n, torch.float32, 3)
+        pages, heads, page, dim = k_codes.shape
+        blocks = k_scales.shape[2]
+        if v_codes.shape != k_codes.shape or v_scales.shape != k_scales.shape:
+            raise ValueError("K and V differ in shape")
+        if k_scales.shape[:2] != (pages, heads) or blocks < 1 or page % blocks:
+            raise ValueError(f"scales {tuple(k_scales.shape)} do not fit codes "
+                             f"{tuple(k_codes.shape)}")
+        if len({t.get_device() for t in (k_codes, v_codes, k_scales, v_scales)}) != 1:
+            raise ValueError("all tensors must be on one device")
+        self.k_codes, self.v_codes, self.k_scales, self.v_scales = (k_codes, v_codes, k_scales,
+                                                                    v_scales)
+        self.num_pages, self.kv_heads, self.page_tokens, self.head_dim = pages, heads, page, dim
+        self.scale_tokens = page // blocks
+        self._c = _CKvCache(k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(),
+                            v_scales.data_ptr(), pages, heads, dim, page, self.scale_tokens)
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def empty(cls, num_pages: int, kv_heads: int, head_dim: int, page_tokens: int = 64,
+              scale_tokens: int = 16, device="cuda") -> "KvCache":
+        """A cache of its own tensors, not cleared (new pages need no clearing)."""
+        if scale_tokens < 1 or page_tokens % scale_tokens:
+            raise ValueError(f"page_tokens {page_tokens} is no multiple of scale_tokens "
+                             f"{scale_tokens}")
+        codes = [torch.empty((num_pages, kv_heads, page_tokens, head_dim), dtype=torch.int8,
+                             device=device) for _ in range(2)]
+        scales = [torch.empty((num_pages, kv_heads, page_tokens // scale_tokens),
+                              dtype=torch.float32, device=device) for _ in range(2)]
+        return cls(*codes, *scales)
+
+
+def _kv_batch(cache: KvCache, q_start, kv_len, page_table, tokens: int) -> _CKvBatch:
+    for t, n, dim in ((q_start, "q_start", 1), (kv_len, "kv_len", 1),
+                      (page_table, "page_table", 2)):
+        _check(t, n, torch.int32, dim)
+    batch = kv_len.shape[0]
+    if q_start.shape[0] != batch + 1 or page_table.shape[0] != batch:
+        raise ValueError(f"kv_len has {batch} sequences, q_start {q_start.shape[0]} entries, "
+                         f"page_table {page_table.shape[0]} rows")
+    return _CKvBatch(q_start.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), batch,
+                     page_table.shape[1], tokens)
+
+
+def _rows(t, name: str, width: int, tokens: int | None = None):
+    """(pointer, row distance in elements) of a bf16 CUDA matrix of `width` columns whose rows may
+    lie apart; [tokens, heads, head_dim] counts as [tokens, heads * head_dim]."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.dim() == 3:
+        if t.shape[0] and t.stride(2) == 1 and t.stride(1) == t.shape[2]:
+            cols = t.shape[1] * t.shape[2]
+        elif t.is_contiguous():
+            cols = t.shape[1] * t.shape[2]
+        else:
+            raise ValueError(f"the heads of a row of {name} must lie one after the other")
+    elif t.dim() == 2:
+        cols = t.shape[1]
+        if cols > 1 and t.stride(1) != 1:
+            raise ValueError(f"the columns of {name} must be contiguous")
+    else:
+        raise ValueError(f"{name} must have 2 or 3 dimensions")
+    if cols != width:
+        raise ValueError(f"{name} has rows of {cols}, {width} wanted")
+    if tokens is not None and t.shape[0] != tokens:
+        raise ValueError(f"{name} has {t.shape[0]} rows, {tokens} wanted")
+    # a single row has no distance to the next one
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else max(width, 8)
+
+
+def bitnet_kv_cache_append(cache: KvCache, K: torch.Tensor, V: torch.Tensor, q_start, kv_len,
+                           page_table, stream=None) -> None:
+    """Quantise the new tokens' K and V (bf16 [tokens, kv_heads * head_dim], rows may lie apart)
+    into the cache.  q_start int32 [batch + 1], kv_len int32 [batch] (with the new tokens),
+    page_table int32 [batch, max_pages]."""
+    L = load_library()
+    width = cache.kv_heads * cache.head_dim
+    k, ldk = _rows(K, "K", width)
+    v, ldv = _rows(V, "V", width, K.shape[0])
+    batch = _kv_batch(cache, q_start, kv_len, page_table, K.shape[0])
+    _same_device(cache.k_codes, K, V, q_start, kv_len, page_table)
+    _rc(L.bitnet_kv_cache_append(cache._ref, ctypes.byref(batch), k, ldk, v, ldv,
+                                 _stream(stream)), "bitnet_kv_cache_append")
+
+
+def bitnet_kv_cache_read(cache: KvCache, tokens: int, q_start, kv_len, page_table, K=None, V=None,
+                         stream=None):
+    """The last q_start[s + 1] - q_start[s] tokens of each sequence as bf16, packed: returns
+    (K, V), each [tokens, kv_heads * head_dim]."""
+    L = load_library()
+    width = cache.kv_heads * cache.head_dim
+    if K is None:
+        K = _empty((tokens, width), torch.bfloat16, cache.k_codes.device, stream)
+    if V is None:
+        V = _empty((tokens, width), torch.bfloat16, cache.k_codes.device, stream)
+    k, ldk = _rows(K, "K", width, tokens)
+    v, ldv = _rows(V, "V", width, tokens)
+    batch = _kv_batch(cache, q_start, kv_len, page_table, tokens)
+    _same_device(cache.k_codes, K, V, q_start, kv_len, page_table)
+    _rc(L.bitnet_kv_cache_read(cache._ref, ctypes.byref(batch), k, ldk, v, ldv, _stream(stream)),
+        "bitnet_kv_cache_read")
+    return K, V
+
+
+def bitnet_kv_attention_workspace_bytes(cache: KvCache, tokens: int, batch: int, max_pages: int,
+                                        q_heads: int, max_new: int) -> int:
+    """Bytes of workspace bitnet_kv_attention needs for such a batch (host only)."""
+    one = 16  # the query looks at sizes, not at the arrays
+    b = _CKvBatch(one, one, one, batch, max_pages, tokens)
+    return int(load_library().bitnet_kv_attention_workspace_bytes(
+        cache._ref, ctypes.byref(b), q_heads, max_new))
+
+
+def bitnet_kv_attention(cache: KvCache, Q: torch.Tensor, q_heads: int, q_start, kv_len,
+                        page_table, max_new: int, scale: float | None = None,
+                        causal: bool = True, Y=None, lse=None, want_lse: bool = False, ws=None,
+                        stream=None):
+    """Attention of new tokens Q (bf16 [tokens, q_heads * head_dim], rows may lie apart) over the
+    cached states of their sequences.  max_new: the most new tokens of any sequence.  scale
+    defaults to 1 / sqrt(head_dim).  Returns (Y bf16 [tokens, q_heads * head_dim], lse float
+    [tokens, q_heads] or None)."""
+    L = load_library()
+    width = q_heads * cache.head_dim
+    q, ldq = _rows(Q, "Q", width)
+    tokens = Q.shape[0]
+    if Y is None:
+        Y = _empty((tokens, width), torch.bfloat16, Q.device, stream)
+    y, ldy = _rows(Y, "Y", width, tokens)
+    if lse is None:
+        if want_lse:
+            lse = _empty((tokens, q_heads), torch.float32, Q.device, stream)
+    else:
+        _check(lse, "lse", torch.float32)
+        _nbytes_at_least(lse, 4 * tokens * q_heads, "lse")
+    batch = _kv_batch(cache, q_start, kv_len, page_table, tokens)
+    ref = ctypes.byref(batch)
+    if ws is None:
+        need = int(L.bitnet_kv_attention_workspace_bytes(cache._ref, ref, q_heads, max_new))
+        if need:
+            ws = _empty(need, torch.uint8, Q.device, stream)
+    else:
+        _check(ws, "ws")
+    _same_device(cache.k_codes, Q, Y, q_start, kv_len, page_table,
+                 *(t for t in (lse, ws) if t is not None))
+    _rc(L.bitnet_kv_attention(cache._ref, ref, q, ldq, q_heads, max_new,
+                              cache.head_dim ** -0.5 if scale is None else float(scale),
+                              int(bool(causal)), y, ldy,
+                              lse.data_ptr() if lse is not None else None,
+                              ws.data_ptr() if ws is not None else None,
+                              ws.numel() * ws.element_size() if ws is not None else 0,
+                              _stream(stream)), "bitnet_kv_attention")
+    return Y, lse
 
 
 def bitnet_selftest_wait_timeout(limit_cycles: int, stream=None) -> None:

@@ -161,10 +161,16 @@ int gemm_impl(DeviceState *st, const void *codes, const float *scales, const int
     return launched(e, n, "ternary_gemm_tc");
 }
 
+// The residual stream of a forward that adds to it first: H = bf16(X + R).
+struct Residual {
+    const void *R;
+    void *H;
+};
+
 int forward_impl(const void *X, int64_t M, int64_t K, const void *Wp, const float *gamma,
                  int64_t N, int act_bits, void *Y, void *ws, size_t ws_bytes, int hadamard,
                  cudaStream_t stream, const NormArgs &nrm = NormArgs(), int activation = 0,
-                 bool absmax4 = false) {
+                 bool absmax4 = false, const Residual *res = nullptr) {
     int rc = check_shape(M, K, N, true, true);
     if (rc) return rc;
     if (act_bits != 8 && act_bits != 4)
@@ -183,9 +189,14 @@ int forward_impl(const void *X, int64_t M, int64_t K, const void *Wp, const floa
     float *scales = reinterpret_cast<float *>(w + round256(bitnet_act_codes_bytes(M, K, act_bits)));
     int32_t *rowsum = reinterpret_cast<int32_t *>(reinterpret_cast<uint8_t *>(scales) +
                                                   round256((size_t)M * sizeof(float)));
-    if ((rc = act_quant_impl(st, X, M, K, hadamard, absmax4 ? kActInt4Absmax : act_bits, codes,
-                             scales, rowsum, nullptr, stream, nrm)))
-        return rc;
+    if (res)
+        rc = launched(launch_residual_norm_quant(X, res->R, M, K, act_bits, nrm, res->H, codes,
+                                                 scales, rowsum, stream),
+                      1, "residual_norm_quant");
+    else
+        rc = act_quant_impl(st, X, M, K, hadamard, absmax4 ? kActInt4Absmax : act_bits, codes,
+                            scales, rowsum, nullptr, stream, nrm);
+    if (rc) return rc;
     // the quantiser above was launched in stream order after whatever wrote Wp
     return gemm_impl(st, codes, scales, rowsum, M, K, Wp, gamma, N, act_bits, nullptr, Y, stream,
                      true, activation);
@@ -370,6 +381,44 @@ int bitnet_norm_bitlinear_forward(const void *X_dev, int64_t M, int64_t K,
     if (rc) return rc;
     return forward_impl(X_dev, M, K, Wp_dev, gamma_dev, N, act_bits, Y_dev, ws_dev, ws_bytes,
                         hadamard ? 1 : 0, reinterpret_cast<cudaStream_t>(stream), nrm);
+}
+
+int bitnet_act_quant_residual_norm(const void *X_dev, const void *R_dev, int64_t M, int64_t K,
+                                   const void *norm_gain_dev, float eps, int act_bits,
+                                   void *H_dev, void *codes_dev, float *scales_dev,
+                                   int32_t *rowsum_dev, bitnet_stream_t stream) {
+    int rc = check_shape(M, K, 8, true, false);
+    if (rc) return rc;
+    if (act_bits != 8 && act_bits != 4)
+        return fail(BITNET_ERR_INVALID, "act_bits = %d must be 8 or 4", act_bits);
+    if (!X_dev || !R_dev || !H_dev || !codes_dev || !scales_dev || !rowsum_dev)
+        return fail(BITNET_ERR_INVALID, "null pointer argument");
+    if (!aligned16(X_dev) || !aligned16(R_dev) || !aligned16(H_dev) || !aligned16(codes_dev))
+        return fail(BITNET_ERR_INVALID, "device pointers must be 16-byte aligned");
+    NormArgs nrm;
+    if ((rc = norm_args(norm_gain_dev, eps, &nrm))) return rc;
+    DeviceState *st = nullptr;
+    if ((rc = device_state(&st))) return rc;
+    return launched(launch_residual_norm_quant(X_dev, R_dev, M, K, act_bits, nrm, H_dev, codes_dev,
+                                               scales_dev, rowsum_dev,
+                                               reinterpret_cast<cudaStream_t>(stream)),
+                    1, "residual_norm_quant");
+}
+
+int bitnet_residual_norm_bitlinear_forward(const void *X_dev, const void *R_dev, int64_t M,
+                                           int64_t K, const void *norm_gain_dev, float eps,
+                                           const void *Wp_dev, const float *gamma_dev, int64_t N,
+                                           int act_bits, void *H_dev, void *Y_dev, void *ws_dev,
+                                           size_t ws_bytes, bitnet_stream_t stream) {
+    NormArgs nrm;
+    int rc = norm_args(norm_gain_dev, eps, &nrm);
+    if (rc) return rc;
+    if (!R_dev || !H_dev) return fail(BITNET_ERR_INVALID, "null pointer argument");
+    if (!aligned16(R_dev) || !aligned16(H_dev))
+        return fail(BITNET_ERR_INVALID, "device pointers must be 16-byte aligned");
+    const Residual res = {R_dev, H_dev};
+    return forward_impl(X_dev, M, K, Wp_dev, gamma_dev, N, act_bits, Y_dev, ws_dev, ws_bytes, 0,
+                        reinterpret_cast<cudaStream_t>(stream), nrm, 0, false, &res);
 }
 
 }  // extern "C"
@@ -699,6 +748,175 @@ int bitnet_quant_states(const void *X_dev, int64_t M, int64_t C, int64_t group, 
     return launched(launch_quant_states(X_dev, M, C, group, bits, codes_dev, scales_dev,
                                         reinterpret_cast<cudaStream_t>(stream)),
                     1, "quant_states");
+}
+
+}  // extern "C"
+
+namespace {
+int log2_of(int64_t v, int lo, int hi) {  // v = 2^result with lo <= result <= hi, else -1
+    const int l = v > 0 && v <= (int64_t(1) << hi) ? log2_exact(v) : -1;
+    return l >= lo ? l : -1;
+}
+
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// The checks that the calls on the cache share; `a` is what the kernels take (status unset).
+int kv_args(const bitnet_kv_cache *c, const bitnet_kv_batch *b, KvArgs *a) {
+    if (!c || !b) return fail(BITNET_ERR_INVALID, "null cache or batch");
+    if (c->kv_heads < 1 || c->kv_heads > 1024)
+        return fail(BITNET_ERR_INVALID, "kv_heads = %d must be in 1 .. 1024", (int)c->kv_heads);
+    if (c->head_dim != 64 && c->head_dim != 128)
+        return fail(BITNET_ERR_UNSUPPORTED, "head_dim = %d must be 64 or 128", (int)c->head_dim);
+    a->page_shift = log2_of(c->page_tokens, 4, 8);
+    if (a->page_shift < 0)
+        return fail(BITNET_ERR_UNSUPPORTED, "page_tokens = %d must be 16, 32, 64, 128 or 256",
+                    (int)c->page_tokens);
+    a->block_shift = log2_of(c->scale_tokens, 4, a->page_shift);
+    if (a->block_shift < 0)
+        return fail(BITNET_ERR_UNSUPPORTED,
+                    "scale_tokens = %d must be a power of two from 16 to page_tokens",
+                    (int)c->scale_tokens);
+    if (c->num_pages < 1 || c->num_pages > INT32_MAX)
+        return fail(BITNET_ERR_INVALID, "num_pages = %lld must be in 1 .. 2^31-1",
+                    (long long)c->num_pages);
+    if (b->batch < 0 || b->batch > (1 << 20) || b->tokens < 0 || b->tokens > (1 << 28))
+        return fail(BITNET_ERR_INVALID, "batch = %lld must be in 0 .. 2^20, tokens = %lld in 0 .. 2^28",
+                    (long long)b->batch, (long long)b->tokens);
+    if (b->max_pages < 1 || b->max_pages > (INT32_MAX >> a->page_shift))
+        return fail(BITNET_ERR_INVALID, "max_pages = %lld must be >= 1 and give positions below 2^31",
+                    (long long)b->max_pages);
+    // a batch of nobody has no arrays
+    if (!c->k_codes || !c->v_codes || !c->k_scales || !c->v_scales ||
+        (b->batch > 0 && (!b->q_start || !b->kv_len || !b->page_table)))
+        return fail(BITNET_ERR_INVALID, "null pointer in the cache or the batch");
+    if (!aligned16(c->k_codes) || !aligned16(c->v_codes))
+        return fail(BITNET_ERR_INVALID, "device pointers must be 16-byte aligned");
+    if (!aligned4(c->k_scales) || !aligned4(c->v_scales) || !aligned4(b->q_start) ||
+        !aligned4(b->kv_len) || !aligned4(b->page_table))
+        return fail(BITNET_ERR_INVALID, "scales and int32 arrays must be 4-byte aligned");
+    a->k_codes = c->k_codes;
+    a->v_codes = c->v_codes;
+    a->k_scales = c->k_scales;
+    a->v_scales = c->v_scales;
+    a->num_pages = (int)c->num_pages;
+    a->kv_heads = c->kv_heads;
+    a->head_dim = c->head_dim;
+    a->q_start = b->q_start;
+    a->kv_len = b->kv_len;
+    a->page_table = b->page_table;
+    a->batch = (int)b->batch;
+    a->max_pages = (int)b->max_pages;
+    a->tokens = (int)b->tokens;
+    a->status = nullptr;
+    return BITNET_OK;
+}
+
+// A bf16 matrix of rows `ld` elements apart, `width` used.
+int check_rows(const void *p, int64_t ld, int64_t width, const char *name) {
+    if (!p) return fail(BITNET_ERR_INVALID, "null pointer argument");
+    if (!aligned16(p)) return fail(BITNET_ERR_INVALID, "device pointers must be 16-byte aligned");
+    if (ld < width || ld % 8 != 0 || ld > (int64_t(1) << 32))
+        return fail(BITNET_ERR_INVALID, "%s rows of %lld elements, %lld apart: the distance must "
+                                        "be a multiple of 8 and at least the row",
+                    name, (long long)width, (long long)ld);
+    return BITNET_OK;
+}
+
+int attention_args(const KvArgs &a, int64_t q_heads, int64_t max_new, AttentionArgs *at) {
+    if (q_heads < a.kv_heads || q_heads % a.kv_heads != 0 || q_heads / a.kv_heads > 128)
+        return fail(BITNET_ERR_INVALID,
+                    "q_heads = %lld must be 1 .. 128 times kv_heads = %d", (long long)q_heads,
+                    a.kv_heads);
+    if (max_new < 1 || max_new > (1 << 28))
+        return fail(BITNET_ERR_INVALID, "max_new = %lld must be in 1 .. 2^28", (long long)max_new);
+    at->q_heads = (int)q_heads;
+    at->max_new = (int)max_new;
+    return BITNET_OK;
+}
+}  // namespace
+
+extern "C" {
+
+int bitnet_kv_cache_append(const bitnet_kv_cache *cache, const bitnet_kv_batch *batch,
+                           const void *K_dev, int64_t ldk, const void *V_dev, int64_t ldv,
+                           bitnet_stream_t stream) {
+    KvArgs a;
+    int rc = kv_args(cache, batch, &a);
+    if (rc) return rc;
+    const int64_t width = (int64_t)a.kv_heads * a.head_dim;
+    if (a.tokens == 0 || a.batch == 0) return BITNET_OK;
+    if ((rc = check_rows(K_dev, ldk, width, "K")) || (rc = check_rows(V_dev, ldv, width, "V")))
+        return rc;
+    DeviceState *st = nullptr;
+    if ((rc = device_state(&st))) return rc;
+    a.status = st->status_word;
+    return launched(launch_kv_append(a, K_dev, ldk, V_dev, ldv,
+                                     reinterpret_cast<cudaStream_t>(stream)),
+                    1, "kv_append");
+}
+
+int bitnet_kv_cache_read(const bitnet_kv_cache *cache, const bitnet_kv_batch *batch, void *K_dev,
+                         int64_t ldk, void *V_dev, int64_t ldv, bitnet_stream_t stream) {
+    KvArgs a;
+    int rc = kv_args(cache, batch, &a);
+    if (rc) return rc;
+    const int64_t width = (int64_t)a.kv_heads * a.head_dim;
+    if (a.tokens == 0 || a.batch == 0) return BITNET_OK;
+    if ((rc = check_rows(K_dev, ldk, width, "K")) || (rc = check_rows(V_dev, ldv, width, "V")))
+        return rc;
+    DeviceState *st = nullptr;
+    if ((rc = device_state(&st))) return rc;
+    a.status = st->status_word;
+    return launched(launch_kv_read(a, K_dev, ldk, V_dev, ldv,
+                                   reinterpret_cast<cudaStream_t>(stream)),
+                    1, "kv_read");
+}
+
+size_t bitnet_kv_attention_workspace_bytes(const bitnet_kv_cache *cache,
+                                           const bitnet_kv_batch *batch, int64_t q_heads,
+                                           int64_t max_new) {
+    KvArgs a;
+    AttentionArgs at;
+    if (kv_args(cache, batch, &a) || attention_args(a, q_heads, max_new, &at)) return 0;
+    return round256(kv_attention_workspace(a, at));
+}
+
+int bitnet_kv_attention(const bitnet_kv_cache *cache, const bitnet_kv_batch *batch,
+                        const void *Q_dev, int64_t ldq, int64_t q_heads, int64_t max_new,
+                        float scale, int causal, void *Y_dev, int64_t ldy, float *lse_dev,
+                        void *ws_dev, size_t ws_bytes, bitnet_stream_t stream) {
+    KvArgs a;
+    AttentionArgs at;
+    int rc = kv_args(cache, batch, &a);
+    if (rc) return rc;
+    if ((rc = attention_args(a, q_heads, max_new, &at))) return rc;
+    if (!(scale > 0.f) || !std::isfinite(scale))
+        return fail(BITNET_ERR_INVALID, "scale = %g must be finite and > 0", (double)scale);
+    if (a.tokens == 0 || a.batch == 0) return BITNET_OK;
+    const int64_t width = q_heads * a.head_dim;
+    if ((rc = check_rows(Q_dev, ldq, width, "Q")) || (rc = check_rows(Y_dev, ldy, width, "Y")))
+        return rc;
+    if (lse_dev && !aligned4(lse_dev))
+        return fail(BITNET_ERR_INVALID, "lse must be 4-byte aligned");
+    const size_t need = round256(kv_attention_workspace(a, at));
+    if (ws_bytes < need)
+        return fail(BITNET_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", ws_bytes, need);
+    if (need && (!ws_dev || !aligned16(ws_dev)))
+        return fail(BITNET_ERR_INVALID, "the workspace must be 16-byte aligned");
+    DeviceState *st = nullptr;
+    if ((rc = device_state(&st))) return rc;
+    a.status = st->status_word;
+    at.Q = Q_dev;
+    at.ldq = ldq;
+    at.scale = scale;
+    at.causal = causal ? 1 : 0;
+    at.Y = Y_dev;
+    at.ldy = ldy;
+    at.lse = lse_dev;
+    int n = 0;
+    const cudaError_t e =
+        launch_kv_attention(a, at, ws_dev, reinterpret_cast<cudaStream_t>(stream), &n);
+    return launched(e, n, "kv_attention");
 }
 
 int bitnet_selftest_wait_timeout(int64_t limit_cycles, bitnet_stream_t stream) {

@@ -58,6 +58,13 @@ cudaError_t launch_act_quant_plain(const void *X, int64_t M, int64_t K, int act_
                                    const NormArgs &nrm, void *codes, float *scales,
                                    int32_t *rowsum, float *zout, cudaStream_t stream);
 
+// Residual addition, RMS normalisation and quantisation in one pass (resnorm.cu): H = bf16(X + R),
+// then the codes of the normalised H.  act_bits 8 or 4 (absmean); nrm.on; K % 128 == 0.  H may be
+// X or R.
+cudaError_t launch_residual_norm_quant(const void *X, const void *R, int64_t M, int64_t K,
+                                       int act_bits, const NormArgs &nrm, void *H, void *codes,
+                                       float *scales, int32_t *rowsum, cudaStream_t stream);
+
 // ---- step 4: product (gemv.cu, gemm_tc.cu) ----
 struct GemmArgs {
     const void *codes;      // int8 [M][K] or packed int4 [M][K/2]
@@ -119,6 +126,37 @@ CUresult encode_tmap_2d(void *encode_fn, CUtensorMap *map, CUtensorMapDataType d
 // fp32 scale per group.  group % 32 == 0, C % group == 0.
 cudaError_t launch_quant_states(const void *X, int64_t M, int64_t C, int64_t group, int bits,
                                 void *codes, float *scales, cudaStream_t stream);
+
+// ---- paged 8-bit K/V cache (kv_cache.cu) and attention over it (kv_attention.cu) ----
+// The cache and batch of include/bitnet.h as the kernels take them.
+struct KvArgs {
+    int8_t *k_codes, *v_codes;  // [num_pages][kv_heads][page][head_dim]
+    float *k_scales, *v_scales;  // [num_pages][kv_heads][page / block]
+    int num_pages, kv_heads, head_dim;
+    int page_shift, block_shift;  // log2 of the tokens of a page and of a scale block
+    const int32_t *q_start, *kv_len, *page_table;
+    int batch, max_pages, tokens;
+    int *status;  // device status word
+};
+cudaError_t launch_kv_append(const KvArgs &a, const void *K, int64_t ldk, const void *V,
+                             int64_t ldv, cudaStream_t stream);
+cudaError_t launch_kv_read(const KvArgs &a, void *K, int64_t ldk, void *V, int64_t ldv,
+                           cudaStream_t stream);
+
+struct AttentionArgs {
+    const void *Q;  // bf16 rows of q_heads * head_dim, ldq elements apart
+    int64_t ldq;
+    int q_heads;
+    int max_new;  // no sequence has more new tokens
+    float scale;
+    int causal;
+    void *Y;  // bf16 rows, ldy elements apart
+    int64_t ldy;
+    float *lse;  // [tokens][q_heads] or nullptr
+};
+size_t kv_attention_workspace(const KvArgs &a, const AttentionArgs &at);
+cudaError_t launch_kv_attention(const KvArgs &a, const AttentionArgs &at, void *ws,
+                                cudaStream_t stream, int *launches);
 
 // ---- failure detection self-test (selftest.cu) ----
 cudaError_t launch_selftest_wait_timeout(long long limit_cycles, int *status,

@@ -1,0 +1,67 @@
+// kv_common.cuh -- what the kernels on the paged 8-bit K/V cache share: the view they are given,
+// and how they find the sequence that a piece of work belongs to.
+#pragma once
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace bitnet {
+
+// The largest s in [0, batch) with begin(s) <= w, by one warp: every step probes 32 places, so a
+// batch of 1024 takes two steps.  begin() is non-decreasing for valid input; whatever it returns,
+// the result is in range (batch >= 1).
+template <class F>
+__device__ __forceinline__ int find_sequence(int64_t w, int batch, F &&begin) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, len = batch;
+    while (len > 1) {
+        const int step = (len + 31) / 32, at = lane * step;
+        const bool before = at < len && (at == 0 || begin(lo + at) <= w);
+        const int hits = __popc(__ballot_sync(0xFFFFFFFFu, before));
+        const int skip = (hits - 1) * step;
+        lo += skip;
+        len = min(step, len - skip);
+    }
+    return lo;
+}
+
+// Rows of one sequence among the packed new tokens, and its cached length.
+struct KvSequence {
+    int first, count, length;  // rows [first, first + count); the length counts them
+    bool valid;
+};
+
+__device__ __forceinline__ KvSequence kv_sequence(const KvArgs &a, int s) {
+    KvSequence q;
+    const int b = __ldg(a.q_start + s), e = __ldg(a.q_start + s + 1);
+    q.first = b;
+    q.length = __ldg(a.kv_len + s);
+    q.valid = b >= 0 && e >= b && e <= a.tokens && q.length >= 0 &&
+              (int64_t)q.length <= (int64_t)a.max_pages << a.page_shift;
+    q.count = q.valid ? e - b : 0;
+    return q;
+}
+
+// Page that holds `position` of sequence s, or -1 (recorded as an invalid argument).
+__device__ __forceinline__ int kv_page(const KvArgs &a, int s, int position) {
+    const int page = __ldg(a.page_table + (int64_t)s * a.max_pages + (position >> a.page_shift));
+    if (page < 0 || page >= a.num_pages) {
+        record_status(a.status, BITNET_ERR_INVALID);
+        return -1;
+    }
+    return page;
+}
+
+// Codes of a position in a page, and the step of its block.
+__device__ __forceinline__ int64_t kv_code_at(const KvArgs &a, int page, int head, int position) {
+    const int in_page = position & ((1 << a.page_shift) - 1);
+    return ((((int64_t)page * a.kv_heads + head) << a.page_shift) + in_page) * a.head_dim;
+}
+
+__device__ __forceinline__ int64_t kv_scale_at(const KvArgs &a, int page, int head, int position) {
+    const int in_page = position & ((1 << a.page_shift) - 1);
+    return (((int64_t)page * a.kv_heads + head) << (a.page_shift - a.block_shift)) +
+           (in_page >> a.block_shift);
+}
+
+}  // namespace bitnet

@@ -155,6 +155,23 @@ int bitnet_act_quant_norm(const void *X_dev, int64_t M, int64_t K, const void *n
                           float eps, int hadamard, int act_bits, void *codes_dev,
                           float *scales_dev, int32_t *rowsum_dev, bitnet_stream_t stream);
 
+/*
+ * The residual stream's step between two sub-layers in one pass: residual addition, the RMS
+ * normalisation above and the activation codes (hadamard == 0: in the published layers the
+ * transform sits in front of Wo and Wdown, whose inputs are no residual streams).  Per token row:
+ *   h = bf16_rn(x + r), stored;  then exactly bitnet_act_quant_norm on h.
+ * The codes equal those of the two separate steps up to near-ties (the sum of squares is taken in
+ * another fp32 order).
+ * X_dev   bf16 [M, K], the sub-layer's output.     R_dev  bf16 [M, K], the residual stream.
+ * H_dev   out: bf16 [M, K], the new residual stream; may be X_dev or R_dev (in place), any other
+ *         overlap is not allowed.
+ * Other arguments, layouts and errors as bitnet_act_quant_norm.
+ */
+int bitnet_act_quant_residual_norm(const void *X_dev, const void *R_dev, int64_t M, int64_t K,
+                                   const void *norm_gain_dev, float eps, int act_bits,
+                                   void *H_dev, void *codes_dev, float *scales_dev,
+                                   int32_t *rowsum_dev, bitnet_stream_t stream);
+
 /* Debug / parity entry: Z = y (hadamard == 0) or (1/sqrt(K)) H_K y (hadamard != 0), float
  * [M, K], with y the normalised rows of bitnet_act_quant_norm (same kernels and arithmetic). */
 int bitnet_norm_transform_f32(const void *X_dev, int64_t M, int64_t K, const void *norm_gain_dev,
@@ -272,6 +289,15 @@ int bitnet_norm_bitlinear_forward(const void *X_dev, int64_t M, int64_t K,
                                   const void *Wp_dev, const float *gamma_dev, int64_t N,
                                   int act_bits, void *Y_dev, void *ws_dev, size_t ws_bytes,
                                   bitnet_stream_t stream);
+
+/* H = bf16_rn(X + R), Y = BitLinear(RMSNorm(H)): the layer behind a residual addition, with the
+ * step of bitnet_act_quant_residual_norm as its quantiser.  Arguments as that call and
+ * bitnet_bitlinear_forward; the same workspace size. */
+int bitnet_residual_norm_bitlinear_forward(const void *X_dev, const void *R_dev, int64_t M,
+                                           int64_t K, const void *norm_gain_dev, float eps,
+                                           const void *Wp_dev, const float *gamma_dev, int64_t N,
+                                           int act_bits, void *H_dev, void *Y_dev, void *ws_dev,
+                                           size_t ws_bytes, bitnet_stream_t stream);
 
 /* Y = act(BitLinear(X)) (hadamard == 0) or act(H-BitLinear(X)): the layer with the activation of
  * bitnet_ternary_gemm_act in its epilogue.  Y is bf16 [M, N] or [M, N/2] (SwiGLU). */
@@ -403,12 +429,113 @@ int bitnet_quant_states(const void *X_dev, int64_t M, int64_t C, int64_t group, 
                         void *codes_dev, float *scales_dev, bitnet_stream_t stream);
 
 /* ---------------------------------------------------------------------------------------- */
+/* Paged 8-bit K / V cache, and attention over it                                           */
+/* ---------------------------------------------------------------------------------------- */
+
+/*
+ * The attention's K and V states kept in 8 bits (BitNet v2 write-up, Tables 2 and 3: the KV cache
+ * in few bits; no layout is printed), with one step for each block of tokens and head.
+ * The caller owns the four arrays; a page holds page_tokens tokens of every head.
+ *   k_codes, v_codes    int8 [num_pages][kv_heads][page_tokens][head_dim], 16-byte aligned
+ *   k_scales, v_scales  float [num_pages][kv_heads][page_tokens / scale_tokens]; a state is
+ *                       code * scale
+ * head_dim is 64 or 128; page_tokens 16, 32, 64, 128 or 256; scale_tokens a power of two from 16
+ * to page_tokens (else BITNET_ERR_UNSUPPORTED).  New pages need no clearing.
+ */
+typedef struct {
+    int8_t *k_codes, *v_codes;
+    float *k_scales, *v_scales;
+    int64_t num_pages;
+    int32_t kv_heads, head_dim, page_tokens, scale_tokens;
+} bitnet_kv_cache;
+
+/*
+ * A batch of sequences and their new tokens, packed one sequence after the other.  The arrays are
+ * int32 on the device, so a captured graph can be replayed with other lengths and pages.
+ *   q_start     [batch + 1]; rows q_start[s] .. q_start[s + 1] - 1 of the token matrices are the
+ *               LAST tokens of sequence s.  Rows before q_start[0] and from q_start[batch] on
+ *               belong to no sequence and stay as they were.
+ *   kv_len      [batch], each sequence's length with its new tokens (0 .. max_pages * page_tokens)
+ *   page_table  [batch][max_pages]; the token at position p lies in page
+ *               page_table[s][p / page_tokens].  Entries behind the length are not read.
+ *   tokens      rows of the token matrices.
+ * What the host cannot see is checked on the device: a sequence whose rows leave 0 .. tokens or
+ * whose length leaves its page table, and a page number outside 0 .. num_pages - 1, make the next
+ * bitnet_sync_status() return BITNET_ERR_INVALID.  Such a sequence is left out (its outputs stay
+ * as they were); such a page is not written, and the tokens of it are not seen by the attention.
+ * tokens == 0 or batch == 0 does nothing.
+ */
+typedef struct {
+    const int32_t *q_start, *kv_len, *page_table;
+    int64_t batch, max_pages, tokens;
+} bitnet_kv_batch;
+
+/*
+ * Writes each sequence's new tokens into the cache.  Per block of scale_tokens tokens and head,
+ * K and V apart, in fp32:
+ *   mx    = max(max |x| over the block's new tokens, 1e-5)
+ *   g_old = 127 * scale, or 0 when the block's first token is new (what a page held before is
+ *           forgotten)
+ *   mx > g_old:  g = mx, scale' = g / 127, the block's older codes c become rint(c * (scale * s));
+ *   else         g = g_old, scale' = scale;
+ *   s = 127 / g,  codes = clip(round_half_even(fl32(x * s)), -127, 127).
+ * A NaN or infinite state makes its block's scale NaN or infinite until the block is begun anew.
+ * K_dev, V_dev  bf16 rows of kv_heads * head_dim states, ldk / ldv elements apart (a multiple of
+ *               8): column slices of a fused Q/K/V product can be passed as they are.
+ * A page that is written belongs to one sequence of the batch; one that several share (a common
+ * prefix) may be read by all.  Two sequences that write to the same page race: codes and scales of
+ * that page are then unspecified.  A sequence with more new tokens than kv_len is invalid.
+ */
+int bitnet_kv_cache_append(const bitnet_kv_cache *cache, const bitnet_kv_batch *batch,
+                           const void *K_dev, int64_t ldk, const void *V_dev, int64_t ldv,
+                           bitnet_stream_t stream);
+
+/*
+ * Reads states back: rows q_start[s] .. q_start[s + 1] - 1 of K_dev and V_dev get the last so many
+ * tokens of sequence s, bf16_rn(code * scale).  Rows of an invalid page stay as they were.  Other
+ * arguments and errors as bitnet_kv_cache_append; the cache is only read.
+ */
+int bitnet_kv_cache_read(const bitnet_kv_cache *cache, const bitnet_kv_batch *batch, void *K_dev,
+                         int64_t ldk, void *V_dev, int64_t ldv, bitnet_stream_t stream);
+
+/*
+ * Attention of the new tokens over their sequences' cached states (write them first with
+ * bitnet_kv_cache_append).  Query head h reads key head h / (q_heads / kv_heads).  With c, d the
+ * cached codes and scales, for the i-th of a sequence's n new tokens:
+ *   s_t = scale * (q . c_K(t)) * d_K(t),   t <= kv_len - n + i (causal != 0) or t < kv_len
+ *   y = sum_t exp(s_t) c_V(t) d_V(t) / sum_t exp(s_t)  (bf16),   lse = log sum_t exp(s_t)  (fp32)
+ * A row that sees no token (a length of 0, or fewer tokens than new ones) gives y = 0, lse = -inf.
+ * The scores are exact products of Q (bf16, scaled by a power of two a row) and the codes, summed
+ * in fp32; the weights are rounded to 11 bits for the product with the V codes, relative to the
+ * row's largest weight; sums are fp32.  Results do not depend on timing.
+ * Q_dev, Y_dev  bf16 rows of q_heads * head_dim, ldq / ldy elements apart (multiples of 8).
+ * q_heads       kv_heads times 1 .. 128.
+ * max_new       no sequence has more new tokens than this (>= 1): it chooses the kernel.  A
+ *               sequence that has more is invalid.
+ * scale         finite and > 0, usually 1 / sqrt(head_dim).
+ * lse_dev       out: float [tokens][q_heads], or NULL.
+ * ws_dev        scratch of ws_bytes >= bitnet_kv_attention_workspace_bytes(...) (0 for arguments
+ *               that are not valid); contents undefined afterwards.  Calls that may overlap need
+ *               a workspace each.
+ */
+size_t bitnet_kv_attention_workspace_bytes(const bitnet_kv_cache *cache,
+                                           const bitnet_kv_batch *batch, int64_t q_heads,
+                                           int64_t max_new);
+
+int bitnet_kv_attention(const bitnet_kv_cache *cache, const bitnet_kv_batch *batch,
+                        const void *Q_dev, int64_t ldq, int64_t q_heads, int64_t max_new,
+                        float scale, int causal, void *Y_dev, int64_t ldy, float *lse_dev,
+                        void *ws_dev, size_t ws_bytes, bitnet_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------- */
 /* Status                                                                                   */
 /* ---------------------------------------------------------------------------------------- */
 
 /* Synchronises `stream`, then returns BITNET_ERR_CUDA if the stream reported a fault,
  * BITNET_ERR_TIMEOUT if a kernel of this library on the current device gave up a bounded
- * wait since the last call (the flag is cleared), else BITNET_OK. */
+ * wait since the last call, BITNET_ERR_INVALID if one met an invalid sequence or page (see
+ * bitnet_kv_batch) -- the first of the two that was recorded; the flag is cleared -- else
+ * BITNET_OK. */
 int bitnet_sync_status(bitnet_stream_t stream);
 
 /*
