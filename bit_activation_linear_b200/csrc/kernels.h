@@ -154,6 +154,12 @@ struct AttentionArgs {
     int64_t ldy;
     float *lse;  // [tokens][q_heads] or nullptr
 };
+// The kernel for prompts (kv_attention_tc.cu) takes more than kDecodeRows rows (new tokens times
+// query heads of a key head), the streaming kernel (kv_attention.cu) the others.
+constexpr int kDecodeRows = 16;
+size_t kv_attention_tc_workspace(const KvArgs &a, const AttentionArgs &at);
+cudaError_t launch_kv_attention_tc(const KvArgs &a, const AttentionArgs &at, void *ws,
+                                   cudaStream_t stream, int *launches);
 size_t kv_attention_workspace(const KvArgs &a, const AttentionArgs &at);
 cudaError_t launch_kv_attention(const KvArgs &a, const AttentionArgs &at, void *ws,
                                 cudaStream_t stream, int *launches);

@@ -1,102 +1,639 @@
-// kv_attention.cu -- attention of new tokens over the paged 8-bit K/V cache.
+// kv_attention.cu -- attention of a few new tokens over the paged 8-bit K/V cache (decoding), and
+// the choice between this kernel and the one for prompts (kv_attention_tc.cu).
 //
 // For a new token at position p of its sequence and query head h of the key head's group:
 //   s_t = scale * d_K(t) * (q . c_K(t)),  t <= p (causal) or t < length
 //   y   = sum_t exp(s_t) d_V(t) c_V(t) / sum_t exp(s_t),   lse = log sum_t exp(s_t)
-// in one pass with a running maximum and sum, all in fp32.  A row that sees nothing gives zeros and
-// lse -inf.
+// With few rows a code is used once or a few times, so the kernel is bound by the stream of codes
+// from HBM: 23 codes per SM and clock at the measured copy rate, which leaves each code about five
+// lane instructions.
 //
-// One warp a row: lanes take tokens for the scores and features for the output.
+// Rows.  The new tokens of a sequence times the query heads of one key head are 8 * NT rows at
+// most; they share every load and conversion of a code.  The products run as
+//   S^T [16 tokens x 8 rows] = K [16 x D] Q^T,   O^T [D x 8 rows] += V^T [D x 16] W^T
+// with mma.m16n8k16, the codes as the 16-row operand: the 8-column operand then wastes little on
+// the rows that are not there.  (tcgen05 would need the converted codes in shared memory: 1 + 1
+// bytes to bring them there and read them, 2 + 2 to write and read the fp16 ones, 6 x 23 bytes a
+// clock, above the 128 that shared memory moves; here it is 2 x 23.)
+//
+// Codes to fp16.  A code c of -128 .. 127 xor 0x80 is the byte c + 128; under the byte 0x64 that is
+// the fp16 number 1152 + c, and one subtraction gives c exactly.  q is scaled by a power of two a
+// row to below 2, so bf16 -> fp16 loses nothing but bits below 2^-24; products are then exact and
+// summed in fp32.  The order of the features inside an mma's k is free, so a lane takes 16
+// consecutive codes of a token with one 16-byte read.
+//
+// Weights.  d_V varies from block to block, so it belongs to the weight: w_t = exp2(s_t log2 e +
+// log2 d_V(t) - m), m the row's maximum of that sum.  w <= 1 is rounded to fp16 (11 bits, or
+// 2^-25 of the row's largest) for the product with the codes; the denominator sums w_t / d_V(t) in
+// fp32, unrounded.  A block is at least 16 tokens, so a chunk of 16 has one d_K and one d_V.
+// m is only moved when a chunk exceeds it by more than 2^8 (the weights then reach 256, far from
+// fp16's limit): nearly all chunks need one vote instead of a reduction and a rescaling.
+//
+// Work split.  Per key head the chunks of all sequences form one line, cut into equal ranges, one
+// for each of P blocks (P * heads fills the SMs once): ragged batches, single long sequences and
+// many short ones all end together.  The ranges are computed from kv_len on the device, so a
+// replayed graph follows its lengths.  A block whose range covers a sequence writes the output;
+// of a sequence that several share, each writes its sums (at most its first and its last piece:
+// two places a block), and a second kernel joins them in a fixed order.
+//
+// In a block each of four warps takes every fourth chunk through its own ring of stages, filled
+// with cp.async (16 bytes a lane) into an xor-swizzled layout: no barrier between the warps, and
+// both kinds of 16-byte reads are free of bank conflicts.
 #include "kv_common.cuh"
 
 namespace bitnet {
 namespace {
 
+constexpr int kWarps = 4;
+constexpr int kStages = 3;
+constexpr int kMinChunks = 32;  // a range shorter than this does not repay the joining
+
+// The device's view of the partial sums: [2 * P][heads][rows][D] sums, then [..][rows][2] maxima
+// and denominators, then one int4 a block: what to join behind it.
+struct Parts {
+    float *sums, *stats;
+    int4 *joins;
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+    return v;
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+// Where the 16-byte piece `c` of token `t` (0 .. 15) lies in a chunk of codes: xor-swizzled so that
+// neither the reads of K (8 lanes: 2 tokens x 4 pieces) nor those of V (8 lanes: 4 tokens x 2
+// pieces; D = 64: 16 lanes of 8 bytes) meet in a bank.
 template <int D>
-__global__ void __launch_bounds__(128)
-    kv_attention_rows_kernel(KvArgs a, AttentionArgs at) {
-    constexpr int F = D / 32;  // features a lane
-    __shared__ float qs[4][D];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t row = (int64_t)blockIdx.x * 4 + warp;
-    if (row >= (int64_t)a.tokens * at.q_heads) return;
-    const int token = (int)(row / at.q_heads), qh = (int)(row - (int64_t)token * at.q_heads);
-    const int s = find_sequence(token, a.batch, [&](int i) { return (int64_t)__ldg(a.q_start + i); });
+__device__ __forceinline__ uint32_t piece(int t, int c) {
+    if constexpr (D == 128) {
+        const int f = ((t & 4) ^ ((t & 1) << 2)) | (t & 2);
+        return (uint32_t)(t * 8 + (c ^ f)) * 16;
+    } else {
+        const int line = t >> 1, slot = (((t & 1) << 2) | c) ^ (2 * (line & 3));
+        return (uint32_t)(line * 8 + slot) * 16;
+    }
+}
+
+__device__ __forceinline__ int chunks_of(int length) {
+    return length > 0 ? (length + kChunk - 1) / kChunk : 1;  // an empty sequence still has outputs
+}
+
+// The length that takes part: 0 for a sequence that is left out.
+__device__ __forceinline__ int work_length(const KvArgs &a, const AttentionArgs &at, int s) {
     const KvSequence q = kv_sequence(a, s);
-    if (!q.valid || q.count > at.max_new) {
-        if (lane == 0) record_status(a.status, BITNET_ERR_INVALID);
+    return q.valid && q.count > 0 && q.count <= at.max_new ? q.length : 0;
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 3)
+    kv_attention_kernel(KvArgs a, AttentionArgs at, Parts parts, int P) {
+    constexpr int ROWS = 8 * NT;
+    constexpr int CB = kChunk * D;           // bytes of a chunk of codes
+    constexpr int STAGE = 2 * CB;            // K and V
+    constexpr int KW = D / 16;               // 4-code words of a token a lane holds = k16 steps
+    constexpr int MT = D / 16;               // 16-feature tiles of O^T
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ float steps[kWarps][kStages][2];
+    __shared__ float red_m[kWarps][ROWS], red_l[kWarps][ROWS];
+    __shared__ long long scan[kWarps];
+    __shared__ int found[4];
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int n = lane >> 2, t = lane & 3;
+    const int head = blockIdx.x / P, p = blockIdx.x - head * P;
+    const int G = at.q_heads / a.kv_heads;
+    pdl_launch_dependents();
+
+    // ---- this block's range of the line of chunks ----
+    // each thread counts a run of sequences; a scan over the threads gives the total and the first
+    // sequence of the range
+    const int run = (a.batch + 32 * kWarps - 1) / (32 * kWarps);
+    const int run0 = min(tid * run, a.batch), run1 = min(run0 + run, a.batch);
+    long long mine = 0;
+    for (int s = run0; s < run1; ++s) mine += chunks_of(work_length(a, at, s));
+    long long upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+        if (lane >= o) upto += v;
+    }
+    if (lane == 31) scan[warp] = upto;
+    __syncthreads();
+    long long total = 0, base = upto - mine;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) base += scan[w];
+        total += scan[w];
+    }
+    const long long workers = min((long long)P, (total + kMinChunks - 1) / kMinChunks);
+    const long long quota = (total + workers - 1) / workers;
+    const long long t0 = p * quota, t1 = min(t0 + quota, total);
+    if (t0 >= t1) {  // nothing left for this block
+        if (head == 0 && tid == 0 && P > 1) parts.joins[p] = make_int4(-1, 0, 0, 0);
         return;
     }
-    const int i = token - q.first;
-    if (i < 0 || i >= q.count) return;  // a row of no sequence
-    const int seen = at.causal ? q.length - q.count + i + 1 : q.length;
-    const int head = qh / (at.q_heads / a.kv_heads);
-    const __nv_bfloat16 *Q = reinterpret_cast<const __nv_bfloat16 *>(at.Q) + token * at.ldq + qh * D;
-    for (int f = lane; f < D; f += 32) qs[warp][f] = __bfloat162float(Q[f]);
-    __syncwarp();
-    float m = -INFINITY, l = 0.f, o[F] = {};
-    for (int t0 = 0; t0 < seen; t0 += 32) {
-        const int t = t0 + lane;
-        float sc = -INFINITY, dv = 0.f;
-        const int8_t *v = nullptr;
-        if (t < seen) {
-            const int page = kv_page(a, s, t);
-            if (page >= 0) {
-                const int64_t c = kv_code_at(a, page, head, t), d = kv_scale_at(a, page, head, t);
-                float dot = 0.f;
-                for (int f = 0; f < D; ++f) dot += qs[warp][f] * (float)a.k_codes[c + f];
-                sc = dot * a.k_scales[d] * at.scale;
-                dv = a.v_scales[d];
-                v = a.v_codes + c;
+    if (mine > 0 && base <= t0 && t0 < base + mine) {
+        int s = run0;
+        for (;; ++s) {
+            const int c = chunks_of(work_length(a, at, s));
+            if (t0 < base + c) break;
+            base += c;
+        }
+        found[0] = s;
+        found[1] = (int)(t0 - base);
+    }
+    __syncthreads();
+    int s = found[0], c0 = found[1];
+    long long at_chunk = t0;  // line position of chunk c0 of sequence s
+    if (head == 0 && tid == 0 && P > 1) parts.joins[p] = make_int4(-1, 0, 0, 0);
+
+    const uint32_t ring = smem_addr(smem) + warp * kStages * STAGE;
+    while (at_chunk < t1) {
+        const KvSequence q = kv_sequence(a, s);
+        const bool out_of_use = !q.valid || q.count > at.max_new;
+        if (out_of_use && tid == 0) record_status(a.status, BITNET_ERR_INVALID);
+        const int length = out_of_use || q.count == 0 ? 0 : q.length;
+        const int rows = out_of_use ? 0 : q.count * G;
+        const int chunks = chunks_of(length);
+        const int c1 = (int)min((long long)chunks, c0 + (t1 - at_chunk));
+        const int real = length > 0 ? c1 : c0;  // an empty sequence's one chunk is not there
+
+        // ---- Q: this lane's features of row n (and n + 8), scaled to below 2 ----
+        uint32_t qf[NT][2 * KW];
+        float rowf[NT][2];  // scale * log2 e / that scaling, rows 2t and 2t + 1
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            const int r = 8 * i + n;
+            uint2 w[KW];
+            uint32_t mx = 0;
+#pragma unroll
+            for (int j = 0; j < KW; ++j) w[j] = make_uint2(0, 0);
+            if (r < rows) {
+                const uint8_t *src = static_cast<const uint8_t *>(at.Q) +
+                                     2 * ((int64_t)(q.first + r / G) * at.ldq +
+                                          (int64_t)(head * G + r % G) * D);
+#pragma unroll
+                for (int j = 0; j < KW / 4; ++j) {
+                    const uint4 *v = reinterpret_cast<const uint4 *>(src + 32 * (t + 4 * j));
+                    const uint4 x = __ldg(v), y = __ldg(v + 1);
+                    w[4 * j] = make_uint2(x.x, x.y);
+                    w[4 * j + 1] = make_uint2(x.z, x.w);
+                    w[4 * j + 2] = make_uint2(y.x, y.y);
+                    w[4 * j + 3] = make_uint2(y.z, y.w);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < KW; ++j)
+                mx = __vmaxu2(__vmaxu2(mx, w[j].x & 0x7FFF7FFFu), w[j].y & 0x7FFF7FFFu);
+            mx = max(mx & 0xFFFFu, mx >> 16);
+            mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+            mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
+            float up, down;
+            row_scaling(mx, down, up);
+#pragma unroll
+            for (int j = 0; j < KW; ++j) {
+                qf[i][2 * j] = half2_of(__uint_as_float(w[j].x << 16) * down,
+                                        __uint_as_float(w[j].x & 0xFFFF0000u) * down);
+                qf[i][2 * j + 1] = half2_of(__uint_as_float(w[j].y << 16) * down,
+                                            __uint_as_float(w[j].y & 0xFFFF0000u) * down);
+            }
+            const float f = up * (at.scale * kLog2e);
+            rowf[i][0] = __shfl_sync(0xFFFFFFFFu, f, 8 * t);
+            rowf[i][1] = __shfl_sync(0xFFFFFFFFu, f, 8 * t + 4);
+        }
+        // what rows 2t, 2t + 1 see; rows that are not there see everything and are dropped
+        int seen[NT][2];
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int r = 8 * i + 2 * t + k;
+                seen[i][k] = at.causal && r < rows ? length - q.count + r / G + 1 : length;
+            }
+        const int all_see = at.causal ? length - q.count + 1 : length;
+
+        float o[NT][MT][4], m[NT][2], l[NT][2];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            m[i][0] = m[i][1] = -INFINITY;
+            l[i][0] = l[i][1] = 0.f;
+#pragma unroll
+            for (int j = 0; j < MT; ++j) o[i][j][0] = o[i][j][1] = o[i][j][2] = o[i][j][3] = 0.f;
+        }
+
+        // ---- the ring ----
+        const int first = c0 + warp;
+        const int count = real > first ? (real - first + kWarps - 1) / kWarps : 0;
+        uint32_t there = 0;  // stages whose page is valid
+        int page = count > 0 ? kv_page(a, s, first * kChunk) : 0;  // of the next chunk to bring in
+        auto bring = [&](int k) {
+            if (k < count) {
+                const int pos = (first + kWarps * k) * kChunk, st = k % kStages;
+                if (page >= 0) {
+                    const uint32_t dst = ring + st * STAGE;
+                    const int64_t at_code = kv_code_at(a, page, head, pos);
+#pragma unroll
+                    for (int i = 0; i < CB / 512; ++i) {
+                        const int x = lane + 32 * i;
+                        const uint32_t d = piece<D>(x / (D / 16), x % (D / 16));
+                        cp_async16(dst + d, a.k_codes + at_code + 16 * x);
+                        cp_async16(dst + CB + d, a.v_codes + at_code + 16 * x);
+                    }
+                    if (lane < 2)
+                        cp_async4(smem_addr(&steps[warp][st][lane]),
+                                  (lane ? a.v_scales : a.k_scales) + kv_scale_at(a, page, head, pos));
+                    there |= 1u << st;
+                } else {
+                    there &= ~(1u << st);
+                }
+                if (k + 1 < count) page = kv_page(a, s, pos + kWarps * kChunk);
+            }
+            cp_async_commit();
+        };
+#pragma unroll
+        for (int k = 0; k < kStages - 1; ++k) bring(k);
+        for (int k = 0; k < count; ++k) {
+            bring(k + kStages - 1);
+            cp_async_wait<kStages - 1>();
+            __syncwarp();
+            const int st = k % kStages, pos = (first + kWarps * k) * kChunk;
+            if (there >> st & 1) {
+                const uint32_t kc = ring + st * STAGE, vc = kc + CB;
+                const float dk = steps[warp][st][0], dv = v_step(steps[warp][st][1]);
+                float sc[NT][4];
+#pragma unroll
+                for (int i = 0; i < NT; ++i) sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.f;
+                // S^T: tokens n and n + 8
+#pragma unroll
+                for (int j = 0; j < KW / 4; ++j) {
+                    const uint4 x = lds128(kc + piece<D>(n, t + 4 * j));
+                    const uint4 y = lds128(kc + piece<D>(n + 8, t + 4 * j));
+                    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t u = xs[e] ^ 0x80808080u, v = ys[e] ^ 0x80808080u;
+                        const uint32_t a0 = codes_lo(u), a1 = codes_lo(v), a2 = codes_hi(u),
+                                       a3 = codes_hi(v);
+#pragma unroll
+                        for (int i = 0; i < NT; ++i)
+                            mma_f16(sc[i], a0, a1, a2, a3, qf[i][2 * (4 * j + e)],
+                                    qf[i][2 * (4 * j + e) + 1]);
+                    }
+                }
+                // V, already on its way while the weights are made
+                uint32_t vw[4][MT / 2];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int tok = 2 * t + (e & 1) + 8 * (e >> 1);
+                    if constexpr (D == 128) {
+                        const uint4 x = lds128(vc + piece<D>(tok, n));
+                        vw[e][0] = x.x; vw[e][1] = x.y; vw[e][2] = x.z; vw[e][3] = x.w;
+                    } else {
+                        const uint2 x = lds64(vc + piece<D>(tok, n >> 1) + (n & 1) * 8);
+                        vw[e][0] = x.x; vw[e][1] = x.y;
+                    }
+                }
+                // weights
+                const float lv = log2_approx(dv), rv = __frcp_rn(dv);
+                uint32_t wt[NT][2];
+                bool over = false;
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    const float f0 = rowf[i][0] * dk, f1 = rowf[i][1] * dk;
+                    sc[i][0] = fmaf(sc[i][0], f0, lv);
+                    sc[i][1] = fmaf(sc[i][1], f1, lv);
+                    sc[i][2] = fmaf(sc[i][2], f0, lv);
+                    sc[i][3] = fmaf(sc[i][3], f1, lv);
+                    if (pos + kChunk > all_see) {
+#pragma unroll
+                        for (int k4 = 0; k4 < 4; ++k4)
+                            if (pos + n + 8 * (k4 >> 1) >= seen[i][k4 & 1]) sc[i][k4] = -INFINITY;
+                    }
+                    over |= fmaxf(sc[i][0], sc[i][2]) > m[i][0] + kSlack ||
+                            fmaxf(sc[i][1], sc[i][3]) > m[i][1] + kSlack;
+                }
+                if (__any_sync(0xFFFFFFFFu, over)) {
+#pragma unroll
+                    for (int i = 0; i < NT; ++i)
+#pragma unroll
+                        for (int k2 = 0; k2 < 2; ++k2) {
+                            float x = fmaxf(sc[i][k2], sc[i][k2 + 2]);
+                            x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
+                            x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
+                            x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
+                            x = fmaxf(x, m[i][k2]);
+                            const float keep = m[i][k2] == -INFINITY ? 0.f : exp2_approx(m[i][k2] - x);
+                            m[i][k2] = x;
+                            l[i][k2] *= keep;
+#pragma unroll
+                            for (int j = 0; j < MT; ++j) {
+                                o[i][j][k2] *= keep;
+                                o[i][j][k2 + 2] *= keep;
+                            }
+                        }
+                }
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    const float m0 = m[i][0] == -INFINITY ? 0.f : m[i][0];
+                    const float m1 = m[i][1] == -INFINITY ? 0.f : m[i][1];
+                    const float w0 = exp2_approx(sc[i][0] - m0), w1 = exp2_approx(sc[i][1] - m1);
+                    const float w2 = exp2_approx(sc[i][2] - m0), w3 = exp2_approx(sc[i][3] - m1);
+                    const float s0 = w0 + w2, s1 = w1 + w3;
+                    // a row that sees none of the chunk takes nothing of it, whatever its step is
+                    if (s0 != 0.f) l[i][0] = fmaf(s0, rv, l[i][0]);
+                    if (s1 != 0.f) l[i][1] = fmaf(s1, rv, l[i][1]);
+                    wt[i][0] = transpose8x8(half2_of(w0, w1));
+                    wt[i][1] = transpose8x8(half2_of(w2, w3));
+                }
+                // O^T += V^T W^T: this lane's features are d = (D / 8) n + 2j (+ 1)
+#pragma unroll
+                for (int e = 0; e < MT / 2; ++e) {
+                    uint32_t f[2][4];  // [token pair][feature 4e ..]
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t u = vw[2 * h][e] ^ 0x80808080u;
+                        const uint32_t v = vw[2 * h + 1][e] ^ 0x80808080u;
+                        const uint32_t x = prmt(u, v, 0x5140u), y = prmt(u, v, 0x7362u);
+                        f[h][0] = codes_lo(x);
+                        f[h][1] = codes_hi(x);
+                        f[h][2] = codes_lo(y);
+                        f[h][3] = codes_hi(y);
+                    }
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) {
+                        mma_f16(o[i][2 * e], f[0][0], f[0][1], f[1][0], f[1][1], wt[i][0], wt[i][1]);
+                        mma_f16(o[i][2 * e + 1], f[0][2], f[0][3], f[1][2], f[1][3], wt[i][0],
+                                wt[i][1]);
+                    }
+                }
+            }
+            __syncwarp();  // the stage may be filled again
+        }
+
+        // ---- join the four warps ----
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                l[i][k] += __shfl_xor_sync(0xFFFFFFFFu, l[i][k], 4);
+                l[i][k] += __shfl_xor_sync(0xFFFFFFFFu, l[i][k], 8);
+                l[i][k] += __shfl_xor_sync(0xFFFFFFFFu, l[i][k], 16);
+                if (n == 0) {
+                    red_m[warp][8 * i + 2 * t + k] = m[i][k];
+                    red_l[warp][8 * i + 2 * t + k] = l[i][k];
+                }
+            }
+        cp_async_wait<0>();
+        __syncthreads();  // every warp has left its ring: it holds the sums now
+        float *acc = reinterpret_cast<float *>(smem);  // [warp][row][D + 4]
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                float *dst = acc + ((warp * ROWS + 8 * i + 2 * t + k) * (D + 4)) + n * (D / 8);
+#pragma unroll
+                for (int j = 0; j < MT; ++j)
+                    *reinterpret_cast<float2 *>(dst + 2 * j) = make_float2(o[i][j][k], o[i][j][k + 2]);
+            }
+        __syncthreads();
+        const bool whole = c0 == 0 && c1 == chunks;
+        const int slot = 2 * p + (at_chunk != t0);
+        for (int x = tid; x < rows * (D / 4); x += 32 * kWarps) {
+            const int r = x / (D / 4), d = (x - r * (D / 4)) * 4;
+            float mr = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) mr = fmaxf(mr, red_m[w][r]);
+            float lr = 0.f;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float keep = red_m[w][r] == -INFINITY ? 0.f : exp2_approx(red_m[w][r] - mr);
+                const float4 u = *reinterpret_cast<const float4 *>(acc + (w * ROWS + r) * (D + 4) + d);
+                // a warp that saw nothing has sums of 0; one whose sums are NaN keeps them
+                lr = fmaf(red_l[w][r], keep, lr);
+                v.x = fmaf(u.x, keep, v.x);
+                v.y = fmaf(u.y, keep, v.y);
+                v.z = fmaf(u.z, keep, v.z);
+                v.w = fmaf(u.w, keep, v.w);
+            }
+            if (whole) {
+                const float inv = lr == 0.f ? 0.f : __fdividef(1.f, lr);
+                const int64_t token = q.first + r / G, qh = head * G + r % G;
+                *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(at.Y) +
+                                           2 * (token * at.ldy + qh * D + d)) =
+                    make_uint2(bf16x2_of(v.x * inv, v.y * inv), bf16x2_of(v.z * inv, v.w * inv));
+                if (at.lse && d == 0)
+                    at.lse[token * at.q_heads + qh] =
+                        lr == 0.f ? -INFINITY : (mr + log2_approx(lr)) * kLn2;
+            } else {
+                const int64_t row = ((int64_t)slot * a.kv_heads + head) * ROWS + r;
+                *reinterpret_cast<float4 *>(parts.sums + row * D + d) = v;
+                if (d == 0) *reinterpret_cast<float2 *>(parts.stats + 2 * row) = make_float2(mr, lr);
             }
         }
-        float mt = sc;
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xFFFFFFFFu, mt, x));
-        const float mn = fmaxf(m, mt);
-        const float base = mn == -INFINITY ? 0.f : mn;
-        const float p = v ? __expf(sc - base) : 0.f, keep = __expf(m - base);
-        float sum = p;
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, x);
-        l = l * keep + sum;
-        m = mn;
-#pragma unroll
-        for (int f = 0; f < F; ++f) o[f] *= keep;
-        for (int j = 0; j < 32; ++j) {
-            const float w = __shfl_sync(0xFFFFFFFFu, v ? p * dv : 0.f, j);
-            const int8_t *vj = reinterpret_cast<const int8_t *>(
-                __shfl_sync(0xFFFFFFFFu, (unsigned long long)v, j));
-            if (vj)
-#pragma unroll
-                for (int f = 0; f < F; ++f) o[f] += w * (float)vj[f * 32 + lane];
-        }
+        // a sequence that begins in this range and ends in a later one is joined behind this block
+        if (head == 0 && tid == 0 && c0 == 0 && c1 < chunks)
+            parts.joins[p] = make_int4(s, (int)((at_chunk + chunks - 1) / quota) - p + 1, slot, 0);
+        __syncthreads();  // the sums have been read: the ring may be filled again
+        at_chunk += c1 - c0;
+        c0 = 0;
+        ++s;
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    __nv_bfloat16 *Y = reinterpret_cast<__nv_bfloat16 *>(at.Y) + token * at.ldy + qh * D;
+}
+
+// Joins the pieces of the sequence that begins in the range of block p and ends in a later one:
+// eight rows of one key head, four warps each, the pieces in turn.
+template <int D, int NT>
+__global__ void __launch_bounds__(1024)
+    kv_attention_join_kernel(KvArgs a, AttentionArgs at, Parts parts, int P) {
+    constexpr int F = D / 32;  // features a lane
+    __shared__ float sums[8][3][D], stats[8][3][2];
+    pdl_wait();
+    const int p = blockIdx.x % P, head = blockIdx.x / P;
+    const int4 join = parts.joins[p];
+    if (join.x < 0) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quarter = warp & 3;
+    const KvSequence q = kv_sequence(a, join.x);
+    const int G = at.q_heads / a.kv_heads, rows = q.count * G;
+    for (int r0 = 0; r0 < 8 * NT; r0 += 8) {
+        const int r = r0 + (warp >> 2);
+        const bool live = r < rows;
+        float m = -INFINITY, l = 0.f, v[F] = {};
+        if (live) {
+#pragma unroll 4
+            for (int i = quarter; i < join.y; i += 4) {
+                const int64_t slot = i == 0 ? join.z : 2 * (p + i);
+                const int64_t row = (slot * a.kv_heads + head) * (8 * NT) + r;
+                const float2 ml = *reinterpret_cast<const float2 *>(parts.stats + 2 * row);
+                float u[F];
+                if constexpr (F == 4) {
+                    const float4 x = *reinterpret_cast<const float4 *>(parts.sums + row * D + 4 * lane);
+                    u[0] = x.x; u[1] = x.y; u[2] = x.z; u[3] = x.w;
+                } else {
+                    const float2 x = *reinterpret_cast<const float2 *>(parts.sums + row * D + 2 * lane);
+                    u[0] = x.x; u[1] = x.y;
+                }
+                const float mn = fmaxf(m, ml.x);
+                const float old = m == -INFINITY ? 0.f : exp2_approx(m - mn);
+                const float now = ml.x == -INFINITY ? 0.f : exp2_approx(ml.x - mn);
+                // with nothing seen the sums are 0, or NaN (which stays) where a step was
+                l = l * old + ml.y * now;
 #pragma unroll
-    for (int f = 0; f < F; ++f) Y[f * 32 + lane] = __float2bfloat16(o[f] * inv);
-    if (at.lse && lane == 0)
-        at.lse[row] = l == 0.f ? -INFINITY : m + logf(l);
+                for (int f = 0; f < F; ++f) v[f] = v[f] * old + u[f] * now;
+                m = mn;
+            }
+        }
+        if (live && quarter) {
+            for (int f = 0; f < F; ++f) sums[warp >> 2][quarter - 1][F * lane + f] = v[f];
+            if (lane == 0) {
+                stats[warp >> 2][quarter - 1][0] = m;
+                stats[warp >> 2][quarter - 1][1] = l;
+            }
+        }
+        __syncthreads();
+        if (live && quarter == 0) {
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+                const float mi = stats[warp >> 2][i][0], li = stats[warp >> 2][i][1];
+                const float mn = fmaxf(m, mi);
+                const float old = m == -INFINITY ? 0.f : exp2_approx(m - mn);
+                const float now = mi == -INFINITY ? 0.f : exp2_approx(mi - mn);
+                l = l * old + li * now;
+#pragma unroll
+                for (int f = 0; f < F; ++f)
+                    v[f] = v[f] * old + sums[warp >> 2][i][F * lane + f] * now;
+                m = mn;
+            }
+            const float inv = l == 0.f ? 0.f : __fdividef(1.f, l);
+            const int64_t token = q.first + r / G, qh = head * G + r % G;
+            uint8_t *Y = static_cast<uint8_t *>(at.Y) + 2 * (token * at.ldy + qh * D + F * lane);
+            uint32_t y[F / 2];
+#pragma unroll
+            for (int f = 0; f < F / 2; ++f)
+                y[f] = bf16x2_of(v[2 * f] * inv, v[2 * f + 1] * inv);
+            if constexpr (F == 4)
+                *reinterpret_cast<uint2 *>(Y) = make_uint2(y[0], y[1]);
+            else
+                *reinterpret_cast<uint32_t *>(Y) = y[0];
+            if (at.lse && lane == 0)
+                at.lse[token * at.q_heads + qh] = l == 0.f ? -INFINITY : (m + log2_approx(l)) * kLn2;
+        }
+        __syncthreads();
+    }
+}
+
+// Rows a sequence and key head can have, as tiles of 8 (0: too many for the kernel above).
+int row_tiles(const KvArgs &a, const AttentionArgs &at) {
+    const int64_t rows = (int64_t)at.max_new * (at.q_heads / a.kv_heads);
+    return rows <= 8 ? 1 : rows <= kDecodeRows ? 2 : 0;
+}
+
+// Blocks per key head: as many as fill the SMs, no more than the longest batch that the page table
+// allows can use.
+int worker_blocks(const KvArgs &a, int nt) {
+    const int64_t fill = kSms * (nt == 1 ? 4 : 3) / a.kv_heads;
+    const int64_t most = ((int64_t)a.batch * ((int64_t)a.max_pages << a.page_shift) / kChunk +
+                          a.batch + kMinChunks - 1) / kMinChunks;
+    const int64_t p = fill < most ? fill : most;
+    return p < 1 ? 1 : (int)p;
+}
+
+size_t part_floats(const KvArgs &a, int nt, int P) {
+    return (size_t)2 * P * a.kv_heads * 8 * nt;  // rows of partial sums
+}
+
+template <int D, int NT>
+cudaError_t launch_decode(const KvArgs &a, const AttentionArgs &at, void *ws, cudaStream_t stream,
+                          int *launches) {
+    const int P = worker_blocks(a, NT);
+    constexpr int ring = kWarps * kStages * 2 * kChunk * D;
+    constexpr int join = kWarps * 8 * NT * (D + 4) * 4;
+    constexpr int smem = ring > join ? ring : join;
+    Parts parts = {};
+    if (P > 1) {
+        const size_t rows = part_floats(a, NT, P);
+        parts.sums = static_cast<float *>(ws);
+        parts.stats = parts.sums + rows * D;
+        parts.joins = reinterpret_cast<int4 *>(parts.stats + rows * 2);
+    }
+    auto kern = kv_attention_kernel<D, NT>;
+    static bool configured[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64 && !configured[dev]) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        configured[dev] = true;
+    }
+    kern<<<(unsigned)(P * a.kv_heads), 32 * kWarps, smem, stream>>>(a, at, parts, P);
+    *launches = 1;
+    if ((e = cudaGetLastError()) != cudaSuccess || P == 1) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(P * a.kv_heads));
+    cfg.blockDim = dim3(1024);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    *launches = 2;
+    return cudaLaunchKernelEx(&cfg, kv_attention_join_kernel<D, NT>, a, at, parts, P);
 }
 
 }  // namespace
 
 size_t kv_attention_workspace(const KvArgs &a, const AttentionArgs &at) {
-    (void)a;
-    (void)at;
-    return 0;
+    const int nt = row_tiles(a, at);
+    if (nt == 0) return kv_attention_tc_workspace(a, at);
+    const int P = worker_blocks(a, nt);
+    return P == 1 ? 0 : part_floats(a, nt, P) * (a.head_dim + 2) * 4 + (size_t)P * sizeof(int4);
 }
 
 cudaError_t launch_kv_attention(const KvArgs &a, const AttentionArgs &at, void *ws,
                                 cudaStream_t stream, int *launches) {
-    (void)ws;
-    const int64_t rows = (int64_t)a.tokens * at.q_heads, blocks = (rows + 3) / 4;
-    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-    *launches = 1;
-    auto kern = a.head_dim == 64 ? kv_attention_rows_kernel<64> : kv_attention_rows_kernel<128>;
-    kern<<<(unsigned)blocks, 128, 0, stream>>>(a, at);
-    return cudaGetLastError();
+    switch (row_tiles(a, at)) {
+        case 1:
+            return a.head_dim == 64 ? launch_decode<64, 1>(a, at, ws, stream, launches)
+                                    : launch_decode<128, 1>(a, at, ws, stream, launches);
+        case 2:
+            return a.head_dim == 64 ? launch_decode<64, 2>(a, at, ws, stream, launches)
+                                    : launch_decode<128, 2>(a, at, ws, stream, launches);
+    }
+    return launch_kv_attention_tc(a, at, ws, stream, launches);
 }
 
 }  // namespace bitnet

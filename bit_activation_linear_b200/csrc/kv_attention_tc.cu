@@ -1,0 +1,621 @@
+// kv_attention_tc.cu -- attention of prompts (more than 16 rows a sequence and key head) over the
+// paged 8-bit K/V cache, on the tensor cores.  The formulas, the way codes become fp16 and the way
+// d_V goes into the weights are those of kv_attention.cu.
+//
+// A block takes 256 rows (new token, query head of the group) of one sequence and key head as two
+// tiles of 128, and walks the cache in steps of 128 tokens:
+//   S_i [128 x 128] = Q_i K^T      tcgen05.mma kind::f16, both operands in shared memory
+//   O_i [128 x D]  += W_i V        weights in tensor memory (operand A), V in shared memory
+// The two tiles alternate, so that one's softmax runs while the tensor cores work for the other.
+//
+// Warps: 0-3 and 4-7 the softmax of tile 0 and 1 (a thread owns a row: no shuffles), 8-11 turn K
+// and V codes into fp16, 12 issues the MMAs.  Codes come straight from global memory
+// into registers one step ahead (16 bytes a load) and leave as 128-byte-swizzled fp16 rows, K as a
+// K-major operand, V (token rows, features contiguous) as an MN-major one: neither is transposed.
+//
+// Tensor memory: S_0, S_1 (128 columns each) and O_0, O_1 (D columns each), all 512 for D = 128.
+// The fp16 weights overwrite the first half of their scores.  The MMAs of one tile execute in the
+// order they are issued: W_i V of step j, then Q_i K^T of step j + 1, so S_i's arrival also says
+// that the O_i before it is complete, and the rare rescaling of O_i needs no barrier of its own.
+//
+// Every wait is bounded; after a time-out (recorded) each role leaves its loop and all meet at the
+// end, where tensor memory is freed.
+#include "kv_common.cuh"
+
+namespace bitnet {
+namespace {
+
+constexpr int kTile = 128;           // rows of an MMA, and tokens of a step
+constexpr int kRows = 2 * kTile;     // rows of a block
+constexpr int kGroups = kTile / kChunk;
+constexpr int kBlockBytes = kTile * 128;  // 128 rows of 64 fp16: one swizzled operand block
+constexpr int kMmaWarp = 12;
+constexpr int kThreads = 13 * 32;
+
+__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                           uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                           uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15])
+        : "memory");
+}
+
+// fp16 x fp16 -> fp32; B K-major, or MN-major (features contiguous)
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn) {
+    return (1u << 4) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) |
+           ((uint32_t)(M >> 4) << 24);
+}
+
+// MN-major operand with the 128-byte swizzle: rows (the product's k) of 64 contiguous elements,
+// eight of them 1024 bytes; the next 64 elements lie kBlockBytes further.
+__device__ __forceinline__ uint64_t smem_desc_mnmajor_sw128(uint32_t addr) {
+    uint64_t d = 0;
+    d |= (uint64_t)((addr >> 4) & 0x3FFF);
+    d |= (uint64_t)(kBlockBytes >> 4) << 16;  // leading: next 64 elements
+    d |= (uint64_t)(1024 >> 4) << 32;         // stride: next eight rows
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
+// Where the sums of a split sequence go: [piece][256 rows][D], then [..][2] maxima and denominators.
+struct TcParts {
+    float *sums, *stats;
+};
+
+struct Shared {
+    uint64_t kfull[2], kfree[2], vfull[2], vfree[2], sfull[2], pfull[2], ofull[2], cfull[4];
+    float4 group[4][kGroups];  // {d_K, log2 d_V, 1 / d_V} of the 16-token groups of a step
+    float rowf[kRows];
+    uint32_t tmem;
+};
+
+__device__ __forceinline__ float max16(const uint32_t *v) {
+    float m = __uint_as_float(v[0]);
+#pragma unroll
+    for (int i = 1; i < kChunk; ++i) m = fmaxf(m, __uint_as_float(v[i]));
+    return m;
+}
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
+        "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    kv_attention_tc_kernel(KvArgs a, AttentionArgs at, TcParts parts, int units, int splits) {
+    constexpr int NB = D / 64;                   // operand blocks of 64 features
+    constexpr int TILE_BYTES = NB * kBlockBytes;
+    constexpr uint32_t ID_S = idesc_f16(kTile, kTile, false), ID_O = idesc_f16(kTile, D, true);
+    extern __shared__ uint8_t raw[];
+    __shared__ Shared sh;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    uint8_t *smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
+    const uint32_t sq = smem_addr(smem), sk = sq + 2 * TILE_BYTES, sv = sk + 2 * TILE_BYTES;
+
+    // ---- which rows: the last (longest, when causal) units first, the heads of one together ----
+    int x = blockIdx.x;
+    const int split = x % splits;
+    x /= splits;
+    const int head = x % a.kv_heads;
+    const int unit = units - 1 - x / a.kv_heads;
+    const int G = at.q_heads / a.kv_heads;
+    // sequence s owns the units from first(s) * G / 256 + s on: room for the tiles of its rows
+    auto begin = [&](int i) { return ((int64_t)__ldg(a.q_start + i) * G >> 8) + (int64_t)i; };
+    const int s = find_sequence(unit, a.batch, begin);
+    const KvSequence q = kv_sequence(a, s);
+    if (!q.valid || q.count > at.max_new) {
+        if (tid == 0) record_status(a.status, BITNET_ERR_INVALID);
+        return;
+    }
+    const int64_t tile = unit - begin(s);
+    const int64_t all_rows = (int64_t)q.count * G;
+    if (tile < 0 || tile * kRows >= all_rows) return;
+    const int64_t r0 = tile * kRows;
+    const int rows = (int)min((int64_t)kRows, all_rows - r0);
+    // tokens that the last row of tile i sees, and the steps that it takes
+    int n[2], seen_first[2];
+    int steps = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        int sees = 0;
+        seen_first[i] = 0;
+        if (rows > i * kTile) {
+            const int64_t last = r0 + min(rows, (i + 1) * kTile) - 1, first = r0 + i * kTile;
+            sees = at.causal ? q.length - q.count + (int)(last / G) + 1 : q.length;
+            seen_first[i] = at.causal ? q.length - q.count + (int)(first / G) + 1 : q.length;
+        }
+        n[i] = sees > 0 ? (sees + kTile - 1) / kTile : 0;
+        steps = max(steps, n[i]);
+    }
+    const int k0 = (int)((int64_t)steps * split / splits);
+    const int k1 = (int)((int64_t)steps * (split + 1) / splits);
+    const int ns = k1 - k0;
+    n[0] = max(min(n[0], k1) - k0, 0);
+    n[1] = max(min(n[1], k1) - k0, 0);
+
+    if (tid == 0) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.kfull[i], 4);
+            mbar_init(&sh.vfull[i], 4);
+            mbar_init(&sh.pfull[i], 4);
+            mbar_init(&sh.kfree[i], 1);
+            mbar_init(&sh.vfree[i], 1);
+            mbar_init(&sh.sfull[i], 1);
+            mbar_init(&sh.ofull[i], 1);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mbar_init(&sh.cfull[i], 1);
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(&sh.tmem, 512);
+        tmem_relinquish();
+    }
+    // ---- Q: a warp a row, scaled by a power of two to below 2, as fp16 ----
+    for (int r = warp; r < kRows; r += kThreads / 32) {
+        uint32_t w[D / 64];
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) w[j] = 0;
+        if (r < rows) {
+            const int64_t row = r0 + r;
+            const uint8_t *src = static_cast<const uint8_t *>(at.Q) +
+                                 2 * ((q.first + row / G) * at.ldq +
+                                      (head * (int64_t)G + row % G) * D);
+            if constexpr (D == 128) {
+                const uint2 v = __ldg(reinterpret_cast<const uint2 *>(src) + lane);
+                w[0] = v.x;
+                w[1] = v.y;
+            } else {
+                w[0] = __ldg(reinterpret_cast<const uint32_t *>(src) + lane);
+            }
+        }
+        uint32_t mx = 0;
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) mx = __vmaxu2(mx, w[j] & 0x7FFF7FFFu);
+        mx = __reduce_max_sync(0xFFFFFFFFu, max(mx & 0xFFFFu, mx >> 16));
+        float up, down;
+        row_scaling(mx, down, up);
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j)
+            w[j] = half2_of(__uint_as_float(w[j] << 16) * down,
+                            __uint_as_float(w[j] & 0xFFFF0000u) * down);
+        const int i = r / kTile, rr = r % kTile;
+        uint8_t *dst = smem + i * TILE_BYTES + rr * 128;
+        if constexpr (D == 128) {  // features 4 lane ..: block lane / 16, 8 bytes
+            const int c = (lane & 15) >> 1;
+            *reinterpret_cast<uint2 *>(dst + (lane >> 4) * kBlockBytes + ((c ^ (rr & 7)) << 4) +
+                                       (lane & 1) * 8) = make_uint2(w[0], w[1]);
+        } else {  // features 2 lane ..
+            const int c = lane >> 2;
+            *reinterpret_cast<uint32_t *>(dst + ((c ^ (rr & 7)) << 4) + (lane & 3) * 4) = w[0];
+        }
+        if (lane == 0) sh.rowf[r] = up * (at.scale * kLog2e);
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    bool ok = true;
+
+    if (warp == kMmaWarp) {
+        // ---- the MMAs, one thread ----
+        if (lane == 0 && ns > 0) {
+            auto scores = [&](int i, int j) {
+                const uint32_t qa = sq + i * TILE_BYTES, kb = sk + (j & 1) * TILE_BYTES;
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    const uint64_t ad = smem_desc_kmajor_sw128(qa + b * kBlockBytes);
+                    const uint64_t bd = smem_desc_kmajor_sw128(kb + b * kBlockBytes);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)  // 16 features, 32 bytes, each
+                        mma_f16_ss(tmem + i * kTile, ad + 2 * e, bd + 2 * e, ID_S, b + e > 0);
+                }
+                mma_commit(&sh.sfull[i]);
+            };
+            auto output = [&](int i, int j) {
+                const uint64_t bd = smem_desc_mnmajor_sw128(sv + (j & 1) * TILE_BYTES);
+#pragma unroll
+                for (int e = 0; e < kTile / 16; ++e)  // 16 tokens: 8 columns of weights, 2 KB of V
+                    mma_f16_ts(tmem + 2 * kTile + i * D, tmem + i * kTile + 8 * e,
+                               bd + (2048 >> 4) * e, ID_O, j + e > 0);
+            };
+            ok = mbar_wait(&sh.kfull[0], 0, a.status);
+            tc_fence_after();
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (ok && n[i] > 0) scores(i, 0);
+            if (ok) mma_commit(&sh.kfree[0]);
+            for (int j = 0; j < ns && ok; ++j) {
+                ok = mbar_wait(&sh.vfull[j & 1], (j >> 1) & 1, a.status);
+                const bool more = j + 1 < ns;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (ok && j < n[i]) {
+                        ok = mbar_wait(&sh.pfull[i], j & 1, a.status);
+                        tc_fence_after();
+                        if (ok) {
+                            output(i, j);
+                            if (j == n[i] - 1) mma_commit(&sh.ofull[i]);
+                        }
+                    }
+                    if (ok && more) {
+                        if (i == 0) {
+                            ok = mbar_wait(&sh.kfull[(j + 1) & 1], ((j + 1) >> 1) & 1, a.status);
+                            tc_fence_after();
+                        }
+                        if (ok && j + 1 < n[i]) scores(i, j + 1);
+                    }
+                }
+                if (ok) {
+                    mma_commit(&sh.vfree[j & 1]);
+                    if (more) mma_commit(&sh.kfree[(j + 1) & 1]);
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp >= 8) {
+        // ---- codes to fp16 ----
+        const int ct = tid - 8 * 32;
+        constexpr int PPT = D / 16;          // 16-code pieces a token
+        constexpr int N = PPT;               // pieces a thread: 128 tokens * PPT / 128
+        constexpr int TPI = kTile / PPT;     // tokens the four warps cover with one piece each
+        uint4 kc[N], vc[N];
+        float gk = 0.f, gv = 0.f;            // steps of group `lane` of warp 8
+        int page = -1;                       // of group `lane` of the step to load
+        auto pages = [&](int j) {
+            const int pos = (k0 + j) * kTile + lane * kChunk;
+            page = lane < kGroups && pos < q.length ? kv_page(a, s, pos) : -1;
+        };
+        auto load = [&](const int8_t *codes, uint4 (&c)[N], int j) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int token = i * TPI + ct / PPT;
+                const int pg = __shfl_sync(0xFFFFFFFFu, page, token / kChunk);
+                c[i] = make_uint4(0, 0, 0, 0);
+                if (pg >= 0)
+                    c[i] = ldg_nc_v4(codes + kv_code_at(a, pg, head, (k0 + j) * kTile + token) +
+                                     16 * (ct % PPT));
+            }
+        };
+        auto load_steps = [&](int j) {
+            if (warp == 8 && page >= 0) {
+                const int64_t at_step = kv_scale_at(a, page, head, (k0 + j) * kTile + lane * kChunk);
+                gk = __ldg(a.k_scales + at_step);
+                gv = v_step(__ldg(a.v_scales + at_step));
+            }
+        };
+        auto store = [&](const uint4 (&c)[N], uint32_t stage) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int token = i * TPI + ct / PPT, pc = ct % PPT;
+                const uint32_t w[4] = {c[i].x ^ 0x80808080u, c[i].y ^ 0x80808080u,
+                                       c[i].z ^ 0x80808080u, c[i].w ^ 0x80808080u};
+                const uint4 lo = make_uint4(codes_lo(w[0]), codes_hi(w[0]), codes_lo(w[1]), codes_hi(w[1]));
+                const uint4 hi = make_uint4(codes_lo(w[2]), codes_hi(w[2]), codes_lo(w[3]), codes_hi(w[3]));
+                // 16 features = two 16-byte places of a row; the upper block's lanes write theirs in
+                // the other order, so that eight lanes meet in no bank
+                const bool swap = pc >= 4;
+                const uint32_t row = stage + (pc >> 2) * kBlockBytes + token * 128;
+                const int place = 2 * (pc & 3);
+                const uint4 f = swap ? hi : lo, g = swap ? lo : hi;
+                const uint32_t af = row + (((place + swap) ^ (token & 7)) << 4);
+                const uint32_t ag = row + (((place + !swap) ^ (token & 7)) << 4);
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(af), "r"(f.x), "r"(f.y),
+                             "r"(f.z), "r"(f.w) : "memory");
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(ag), "r"(g.x), "r"(g.y),
+                             "r"(g.z), "r"(g.w) : "memory");
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+        };
+        pages(0);
+        if (ns > 0) {
+            load(a.k_codes, kc, 0);
+            load(a.v_codes, vc, 0);
+            load_steps(0);
+        }
+        for (int j = 0; j < ns; ++j) {
+            const int st = j & 1;
+            if (j >= 2) ok = mbar_wait(&sh.kfree[st], ((j - 2) >> 1) & 1, a.status);
+            if (!__all_sync(0xFFFFFFFFu, ok)) break;
+            if (warp == 8) {
+                // a group behind the length or of an invalid page weighs nothing
+                if (lane < kGroups)
+                    sh.group[j & 3][lane] = page >= 0
+                                                ? make_float4(gk, log2_approx(gv), __frcp_rn(gv), 0.f)
+                                                : make_float4(0.f, -INFINITY, 0.f, 0.f);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.cfull[j & 3]);
+            }
+            store(kc, sk + st * TILE_BYTES);
+            if (lane == 0) mbar_arrive(&sh.kfull[st]);
+            if (j + 1 < ns) {
+                pages(j + 1);
+                load(a.k_codes, kc, j + 1);
+                load_steps(j + 1);
+            }
+            if (j >= 2) ok = mbar_wait(&sh.vfree[st], ((j - 2) >> 1) & 1, a.status);
+            if (!__all_sync(0xFFFFFFFFu, ok)) break;
+            store(vc, sv + st * TILE_BYTES);
+            if (lane == 0) mbar_arrive(&sh.vfull[st]);
+            if (j + 1 < ns) load(a.v_codes, vc, j + 1);
+        }
+    } else {
+        // ---- softmax: thread = row ----
+        const int i = warp >> 2;
+        const int r = i * kTile + (warp & 3) * 32 + lane;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + i * kTile + lanes, to = tmem + 2 * kTile + i * D + lanes;
+        const float rowf = sh.rowf[r];
+        const int64_t row = r0 + r;
+        const bool live = r < rows;
+        // rows that are not there see everything and are dropped
+        const int seen = !live ? INT32_MAX : at.causal ? q.length - q.count + (int)(row / G) + 1 : q.length;
+        float m = -INFINITY, l = 0.f;
+        const int ni = i ? n[1] : n[0], all_see = i ? seen_first[1] : seen_first[0];
+        for (int j = 0; j < ni; ++j) {
+            ok = mbar_wait(&sh.cfull[j & 3], (j >> 2) & 1, a.status) &&
+                 mbar_wait(&sh.sfull[i], j & 1, a.status);
+            if (!__all_sync(0xFFFFFFFFu, ok)) break;
+            tc_fence_after();
+            const float4 *group = sh.group[j & 3];
+            const int pos = (k0 + j) * kTile;
+            const bool masked = pos + kTile > all_see;
+            // the row's largest score * log2 e + log2 d_V
+            float top = -INFINITY;
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                uint32_t v[32];
+                tmem_ld_32x32b_x32(ts + 32 * b, v);
+                tmem_wait_ld();
+                if (masked) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (pos + 32 * b + e >= seen) v[e] = 0xFF800000u;
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float4 g = group[2 * b + h];
+                    top = fmaxf(top, fmaf(max16(v + 16 * h), rowf * g.x, g.y));
+                }
+            }
+            const bool over = top > m + kSlack;
+            if (__any_sync(0xFFFFFFFFu, over)) {
+                const float mn = fmaxf(m, top);
+                const float keep = m == -INFINITY ? 0.f : exp2_approx(m - mn);
+                m = mn;
+                l *= keep;
+                if (j > 0) {
+#pragma unroll
+                    for (int b = 0; b < D / 32; ++b) {
+                        uint32_t v[32];
+                        tmem_ld_32x32b_x32(to + 32 * b, v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            v[e] = __float_as_uint(__uint_as_float(v[e]) * keep);
+                        tmem_st_32x32b_x32(to + 32 * b, v);
+                    }
+                }
+            }
+            const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                uint32_t v[32], w[16];
+                tmem_ld_32x32b_x32(ts + 32 * b, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float4 g = group[2 * b + h];
+                    const float f = rowf * g.x, c = g.y - base;
+                    float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int e = 0; e < 16; e += 2) {
+                        float2 z = fma2(make_float2(__uint_as_float(v[16 * h + e]),
+                                                    __uint_as_float(v[16 * h + e + 1])),
+                                        make_float2(f, f), make_float2(c, c));
+                        z.x = exp2_approx(z.x);
+                        z.y = exp2_approx(z.y);
+                        if (masked) {
+                            if (pos + 32 * b + 16 * h + e >= seen) z.x = 0.f;
+                            if (pos + 32 * b + 16 * h + e + 1 >= seen) z.y = 0.f;
+                        }
+                        sum = add2_rn(sum, z);
+                        w[8 * h + e / 2] = half2_of(z.x, z.y);
+                    }
+                    const float sg = sum.x + sum.y;
+                    // a row that sees none of the group takes nothing of it, whatever its step is
+                    if (sg != 0.f) l = fmaf(sg, g.z, l);
+                }
+                tmem_st_32x32b_x16(ts + 16 * b, w);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.pfull[i]);
+        }
+        // ---- out ----
+        if (ni > 0 && ok) ok = mbar_wait(&sh.ofull[i], 0, a.status);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        tc_fence_after();
+        const int64_t token = q.first + row / G, qh = head * (int64_t)G + row % G;
+        const float inv = l == 0.f ? 0.f : __fdividef(1.f, l);
+        const int64_t piece = (((int64_t)unit * a.kv_heads + head) * splits + split) * kRows + r;
+        if (ok) {
+#pragma unroll
+            for (int b = 0; b < D / 32; ++b) {
+                uint32_t v[32];
+                if (ni > 0) {
+                    tmem_ld_32x32b_x32(to + 32 * b, v);
+                    tmem_wait_ld();
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = 0;
+                }
+                if (!live) continue;
+                if (splits == 1) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(at.Y) +
+                                                           2 * (token * at.ldy + qh * D + 32 * b));
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t y[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            y[k] = bf16x2_of(__uint_as_float(v[8 * e + 2 * k]) * inv,
+                                             __uint_as_float(v[8 * e + 2 * k + 1]) * inv);
+                        dst[e] = make_uint4(y[0], y[1], y[2], y[3]);
+                    }
+                } else {
+                    uint4 *dst = reinterpret_cast<uint4 *>(parts.sums + piece * D + 32 * b);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        dst[e] = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                }
+            }
+            if (live) {
+                if (splits > 1)
+                    *reinterpret_cast<float2 *>(parts.stats + 2 * piece) = make_float2(m, l);
+                else if (at.lse)
+                    at.lse[token * at.q_heads + qh] =
+                        l == 0.f ? -INFINITY : (m + log2_approx(l)) * kLn2;
+            }
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// Joins the pieces of split rows: a warp a row.
+template <int D>
+__global__ void __launch_bounds__(256)
+    kv_attention_tc_join_kernel(KvArgs a, AttentionArgs at, TcParts parts, int units, int splits) {
+    constexpr int F = D / 32;
+    const int lane = threadIdx.x & 31;
+    const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int r = (int)(w % kRows);
+    const int64_t uh = w / kRows;
+    const int head = (int)(uh % a.kv_heads), unit = (int)(uh / a.kv_heads);
+    if (unit >= units) return;
+    const int G = at.q_heads / a.kv_heads;
+    auto begin = [&](int i) { return ((int64_t)__ldg(a.q_start + i) * G >> 8) + (int64_t)i; };
+    const int s = find_sequence(unit, a.batch, begin);
+    const KvSequence q = kv_sequence(a, s);
+    if (!q.valid || q.count > at.max_new) return;
+    const int64_t row = (unit - begin(s)) * kRows + r;
+    if (row < 0 || row >= (int64_t)q.count * G) return;
+    float m = -INFINITY, l = 0.f, v[F] = {};
+#pragma unroll 4
+    for (int i = 0; i < splits; ++i) {
+        const int64_t piece = (uh * splits + i) * kRows + r;
+        const float2 ml = *reinterpret_cast<const float2 *>(parts.stats + 2 * piece);
+        const float mn = fmaxf(m, ml.x);
+        const float old = m == -INFINITY ? 0.f : exp2_approx(m - mn);
+        const float now = ml.x == -INFINITY ? 0.f : exp2_approx(ml.x - mn);
+        l = l * old + ml.y * now;
+#pragma unroll
+        for (int f = 0; f < F; ++f) v[f] = v[f] * old + parts.sums[piece * D + 32 * f + lane] * now;
+        m = mn;
+    }
+    const float inv = l == 0.f ? 0.f : __fdividef(1.f, l);
+    const int64_t token = q.first + row / G, qh = head * (int64_t)G + row % G;
+    __nv_bfloat16 *Y = static_cast<__nv_bfloat16 *>(at.Y) + token * at.ldy + qh * D;
+#pragma unroll
+    for (int f = 0; f < F; ++f) Y[32 * f + lane] = __float2bfloat16(v[f] * inv);
+    if (at.lse && lane == 0)
+        at.lse[token * at.q_heads + qh] = l == 0.f ? -INFINITY : (m + log2_approx(l)) * kLn2;
+}
+
+int64_t tc_units(const KvArgs &a, const AttentionArgs &at) {
+    return ((int64_t)a.tokens * (at.q_heads / a.kv_heads) >> 8) + a.batch;
+}
+
+// Pieces that a row's cache is cut into: enough to fill the SMs, none shorter than four steps of
+// the longest sequence that the page table allows.
+int tc_splits(const KvArgs &a, const AttentionArgs &at) {
+    const int64_t blocks = tc_units(a, at) * a.kv_heads;
+    const int64_t steps = ((int64_t)a.max_pages << a.page_shift) / kTile;
+    int64_t n = kSms / (blocks < 1 ? 1 : blocks);
+    if (n > steps / 4) n = steps / 4;
+    return n < 1 ? 1 : (int)n;
+}
+
+template <int D>
+cudaError_t launch_tc(const KvArgs &a, const AttentionArgs &at, void *ws, cudaStream_t stream,
+                      int *launches) {
+    const int64_t units = tc_units(a, at);
+    const int splits = tc_splits(a, at);
+    const int64_t blocks = units * a.kv_heads * splits;
+    if (units > INT32_MAX || blocks > INT32_MAX) return cudaErrorInvalidValue;
+    constexpr int smem = 6 * (D / 64) * kBlockBytes + 1024;
+    TcParts parts = {};
+    if (splits > 1) {
+        parts.sums = static_cast<float *>(ws);
+        parts.stats = parts.sums + (size_t)blocks * kRows * D;
+    }
+    auto kern = kv_attention_tc_kernel<D>;
+    static bool configured[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64 && !configured[dev]) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        configured[dev] = true;
+    }
+    kern<<<(unsigned)blocks, kThreads, smem, stream>>>(a, at, parts, (int)units, splits);
+    *launches = 1;
+    if ((e = cudaGetLastError()) != cudaSuccess || splits == 1) return e;
+    kv_attention_tc_join_kernel<D><<<(unsigned)(units * a.kv_heads * (kRows / 8)), 256, 0, stream>>>(
+        a, at, parts, (int)units, splits);
+    *launches = 2;
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t kv_attention_tc_workspace(const KvArgs &a, const AttentionArgs &at) {
+    const int splits = tc_splits(a, at);
+    if (splits == 1) return 0;
+    return (size_t)(tc_units(a, at) * a.kv_heads * splits) * kRows * (a.head_dim + 2) * 4;
+}
+
+cudaError_t launch_kv_attention_tc(const KvArgs &a, const AttentionArgs &at, void *ws,
+                                   cudaStream_t stream, int *launches) {
+    return a.head_dim == 64 ? launch_tc<64>(a, at, ws, stream, launches)
+                            : launch_tc<128>(a, at, ws, stream, launches);
+}
+
+}  // namespace bitnet

@@ -64,4 +64,55 @@ __device__ __forceinline__ int64_t kv_scale_at(const KvArgs &a, int page, int he
            (in_page >> a.block_shift);
 }
 
+// ------------------------------------------------------------------------------------------
+// What the attention kernels share
+// ------------------------------------------------------------------------------------------
+constexpr int kChunk = 16;      // tokens: a scale block is a whole number of chunks
+constexpr int kSms = 148;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kSlack = 8.f;   // log2 of how far a weight may exceed 1 before the maximum moves
+
+__device__ __forceinline__ uint32_t sub_1152(uint32_t two) {
+    uint32_t d;
+    asm("sub.f16x2 %0, %1, %2;" : "=r"(d) : "r"(two), "r"(0x64806480u));
+    return d;
+}
+// Bytes 0 and 1, or 2 and 3, of c + 128 as two fp16 numbers c.
+__device__ __forceinline__ uint32_t codes_lo(uint32_t u) { return sub_1152(prmt(u, 0x64646464u, 0x4140u)); }
+__device__ __forceinline__ uint32_t codes_hi(uint32_t u) { return sub_1152(prmt(u, 0x64646464u, 0x4342u)); }
+
+__device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float log2_approx(float x) {
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// bf16 pairs of a row of Q (largest magnitude `mx` as bf16 bits): the powers of two that scale it to
+// below 2 and back; 1 for zeros, infinities and NaN (such a row's outputs are NaN).
+__device__ __forceinline__ void row_scaling(uint32_t mx, float &down, float &up) {
+    const uint32_t ex = mx >> 7;
+    up = mx != 0 && ex < 255 ? __uint_as_float(max(ex, 1u) << 23) : 1.f;
+    down = 1.f / up;
+}
+
+// d_V as the weights carry it: never 0 (a log2 is taken of it), NaN and infinity as they are.
+__device__ __forceinline__ float v_step(float d) { return d < 1e-30f ? 1e-30f : d; }
+
+__device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
 }  // namespace bitnet
