@@ -686,16 +686,34 @@ def bitnet_quant_states(X: torch.Tensor, group: int, bits: int = 3, codes=None, 
     return codes, scales
 
 
-def _same_device(*tensors):
-    """The one device of these CUDA tensors, which has to be the current one: the library launches
-    on the current device."""
-    index = tensors[0].get_device()
-    for t in tensors:
-        if t.get_device() != index:
-            raise ValueError("all tensors must be on one device")
-    if index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on cuda:{index}, the current device is "
+def _device_of(t, name: str) -> int:
+    """The CUDA device of a tensor, which has to be the current one: the library launches there."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name} is on cuda:{dev}, the current device is "
                          f"cuda:{torch.cuda.current_device()}")
+    return dev
+
+
+def _plain(t, name: str, dtype, dim, dev: int) -> int:
+    """The address of a contiguous tensor of this type on device `dev`."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and (dim is None or t.dim() == dim)
+            and t.get_device() == dev and t.is_contiguous()):
+        _check(t, name, dtype, dim)  # says what is wrong
+        raise ValueError("all tensors must be on one device")
+    return t.data_ptr()
+
+
+# the current stream's handle without a Stream object around it (a microsecond and a half)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_on(stream, dev: int) -> int:
+    return _raw_stream(dev) if stream is None and _raw_stream is not None else _stream(stream)
 
 
 def _empty(shape, dtype, device, stream):
@@ -710,43 +728,53 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _residual_args(X, R, norm_gain, H, stream):
+    """Checked (device, M, K, pointers of X, R and the gain, H)."""
+    dev = _device_of(X, "X")
+    x = _plain(X, "X", torch.bfloat16, 2, dev)
+    r = _plain(R, "R", torch.bfloat16, 2, dev)
+    if R.shape != X.shape:
+        raise ValueError(f"R is {tuple(R.shape)}, X is {tuple(X.shape)}")
+    M, K = X.shape
+    gain = None
+    if norm_gain is not None:
+        gain = _plain(norm_gain, "norm_gain", torch.bfloat16, 1, dev)
+        if norm_gain.shape[0] != K:
+            raise ValueError(f"norm_gain has {norm_gain.numel()} entries, K = {K}")
+    if H is None:
+        H = X.new_empty((M, K)) if stream is None else _empty((M, K), X.dtype, X.device, stream)
+    else:
+        _plain(H, "H", torch.bfloat16, None, dev)
+        _nbytes_at_least(H, 2 * M * K, "H")
+    return dev, M, K, x, r, gain, H
+
+
 def bitnet_act_quant_residual_norm(X: torch.Tensor, R: torch.Tensor, norm_gain, eps: float,
                                    act_bits: int, H=None, codes=None, scales=None, rowsum=None,
                                    stream=None):
     """Residual addition, RMS normalisation and per-token quantisation in one pass: H = X + R
     (bf16; may be X or R), codes of the normalised H.  Returns (H, codes, scales, rowsum)."""
-    L = load_library()
-    _check(X, "X", torch.bfloat16, 2)
-    _check(R, "R", torch.bfloat16, 2)
-    M, K = X.shape
-    if R.shape != X.shape:
-        raise ValueError(f"R is {tuple(R.shape)}, X is {tuple(X.shape)}")
-    if H is None:
-        H = _empty((M, K), torch.bfloat16, X.device, stream)
-    else:
-        _check(H, "H", torch.bfloat16)
-        _nbytes_at_least(H, 2 * M * K, "H")
+    L = _lib or load_library()
+    dev, M, K, x, r, gain, H = _residual_args(X, R, norm_gain, H, stream)
     if codes is None:
         codes = _empty((M, K if act_bits == 8 else K // 2),
                        torch.int8 if act_bits == 8 else torch.uint8, X.device, stream)
     else:
-        _check(codes, "codes")
+        _plain(codes, "codes", codes.dtype, None, dev)
         _nbytes_at_least(codes, int(L.bitnet_act_codes_bytes(M, K, act_bits)), "codes")
     if scales is None:
         scales = _empty(M, torch.float32, X.device, stream)
     else:
-        _check(scales, "scales", torch.float32)
+        _plain(scales, "scales", torch.float32, None, dev)
         _nbytes_at_least(scales, 4 * M, "scales")
     if rowsum is None:
         rowsum = _empty(M, torch.int32, X.device, stream)
     else:
-        _check(rowsum, "rowsum", torch.int32)
+        _plain(rowsum, "rowsum", torch.int32, None, dev)
         _nbytes_at_least(rowsum, 4 * M, "rowsum")
-    gain = _gain_ptr(norm_gain, K)
-    _same_device(X, R, H, codes, scales, rowsum, *(() if norm_gain is None else (norm_gain,)))
-    _rc(L.bitnet_act_quant_residual_norm(X.data_ptr(), R.data_ptr(), M, K, gain, float(eps),
-                                         int(act_bits), H.data_ptr(), codes.data_ptr(),
-                                         scales.data_ptr(), rowsum.data_ptr(), _stream(stream)),
+    _rc(L.bitnet_act_quant_residual_norm(x, r, M, K, gain, eps, act_bits, H.data_ptr(),
+                                         codes.data_ptr(), scales.data_ptr(), rowsum.data_ptr(),
+                                         _stream_on(stream, dev)),
         "bitnet_act_quant_residual_norm")
     return H, codes, scales, rowsum
 
@@ -754,37 +782,25 @@ def bitnet_act_quant_residual_norm(X: torch.Tensor, R: torch.Tensor, norm_gain, 
 def bitnet_residual_norm_bitlinear_forward(X, R, norm_gain, eps, Wp, gamma, act_bits=8, H=None,
                                            Y=None, ws=None, stream=None):
     """H = X + R (bf16; may be X or R), Y = BitLinear(RMSNorm(H)).  Returns (H, Y)."""
-    L = load_library()
-    _check(X, "X", torch.bfloat16, 2)
-    _check(R, "R", torch.bfloat16, 2)
-    _check(Wp, "Wp")
-    _check(gamma, "gamma", torch.float32)
-    M, K = X.shape
+    L = _lib or load_library()
+    dev, M, K, x, r, gain, H = _residual_args(X, R, norm_gain, H, stream)
+    wp = _plain(Wp, "Wp", Wp.dtype, None, dev)
+    g = _plain(gamma, "gamma", torch.float32, None, dev)
     N = Wp.shape[0]
-    if R.shape != X.shape:
-        raise ValueError(f"R is {tuple(R.shape)}, X is {tuple(X.shape)}")
-    _nbytes_at_least(Wp, int(L.bitnet_packed_weight_bytes(N, K)), "Wp")
-    if H is None:
-        H = _empty((M, K), torch.bfloat16, X.device, stream)
-    else:
-        _check(H, "H", torch.bfloat16)
-        _nbytes_at_least(H, 2 * M * K, "H")
+    _nbytes_at_least(Wp, N * K // 4, "Wp")
     if Y is None:
         Y = _empty((M, N), torch.bfloat16, X.device, stream)
     else:
-        _check(Y, "Y", torch.bfloat16)
+        _plain(Y, "Y", torch.bfloat16, None, dev)
         _nbytes_at_least(Y, 2 * M * N, "Y")
-    need = int(L.bitnet_workspace_bytes(M, K, N, act_bits))
     if ws is None:
-        ws = _empty(max(need, 256), torch.uint8, X.device, stream)
+        ws = _empty(max(int(L.bitnet_workspace_bytes(M, K, N, act_bits)), 256), torch.uint8,
+                    X.device, stream)
     else:
-        _check(ws, "ws")
-    gain = _gain_ptr(norm_gain, K)
-    _same_device(X, R, Wp, gamma, H, Y, ws, *(() if norm_gain is None else (norm_gain,)))
+        _plain(ws, "ws", ws.dtype, None, dev)
     _rc(L.bitnet_residual_norm_bitlinear_forward(
-        X.data_ptr(), R.data_ptr(), M, K, gain, float(eps), Wp.data_ptr(), gamma.data_ptr(), N,
-        int(act_bits), H.data_ptr(), Y.data_ptr(), ws.data_ptr(),
-        ws.numel() * ws.element_size(), _stream(stream)),
+        x, r, M, K, gain, eps, wp, g, N, act_bits, H.data_ptr(), Y.data_ptr(), ws.data_ptr(),
+        ws.numel() * ws.element_size(), _stream_on(stream, dev)),
         "bitnet_residual_norm_bitlinear_forward")
     return H, Y
 
@@ -795,7 +811,7 @@ class KvCache:
     [num_pages, kv_heads, page_tokens / scale_tokens].  It only holds and describes them."""
 
     __slots__ = ("k_codes", "v_codes", "k_scales", "v_scales", "num_pages", "kv_heads",
-                 "page_tokens", "head_dim", "scale_tokens", "_c", "_ref")
+                 "page_tokens", "head_dim", "scale_tokens", "device", "_c", "_ref", "_sizes")
 
     def __init__(self, k_codes, v_codes, k_scales, v_scales):
         for t, n in ((k_codes, "k_codes"), (v_codes, "v_codes")):
@@ -818,6 +834,8 @@ class KvCache:
         self._c = _CKvCache(k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(),
                             v_scales.data_ptr(), pages, heads, dim, page, self.scale_tokens)
         self._ref = ctypes.byref(self._c)
+        self.device = k_codes.get_device()
+        self._sizes = {}  # workspace bytes by the sizes of a batch
 
     @classmethod
     def empty(cls, num_pages: int, kv_heads: int, head_dim: int, page_tokens: int = 64,
@@ -834,45 +852,48 @@ class KvCache:
 
 
 def _kv_batch(cache: KvCache, q_start, kv_len, page_table, tokens: int) -> _CKvBatch:
-    for t, n, dim in ((q_start, "q_start", 1), (kv_len, "kv_len", 1),
-                      (page_table, "page_table", 2)):
-        _check(t, n, torch.int32, dim)
+    dev, i32 = cache.device, torch.int32
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"the cache is on cuda:{dev}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    starts = _plain(q_start, "q_start", i32, 1, dev)
+    lengths = _plain(kv_len, "kv_len", i32, 1, dev)
+    table = _plain(page_table, "page_table", i32, 2, dev)
     batch = kv_len.shape[0]
-    if q_start.shape[0] != batch + 1 or page_table.shape[0] != batch:
+    rows, max_pages = page_table.shape
+    if q_start.shape[0] != batch + 1 or rows != batch:
         raise ValueError(f"kv_len has {batch} sequences, q_start {q_start.shape[0]} entries, "
-                         f"page_table {page_table.shape[0]} rows")
-    return _CKvBatch(q_start.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), batch,
-                     page_table.shape[1], tokens)
+                         f"page_table {rows} rows")
+    return _CKvBatch(starts, lengths, table, batch, max_pages, tokens)
 
 
-def _rows(t, name: str, width: int, tokens: int | None = None):
-    """(pointer, row distance in elements) of a bf16 CUDA matrix of `width` columns whose rows may
-    lie apart; [tokens, heads, head_dim] counts as [tokens, heads * head_dim]."""
+def _rows(t, name: str, width: int, tokens, dev: int):
+    """(pointer, row distance in elements) of a bf16 matrix of `width` columns on device `dev` whose
+    rows may lie apart; [tokens, heads, head_dim] counts as [tokens, heads * head_dim]."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
+    if t.get_device() != dev:
+        raise ValueError("all tensors must be on one device" if t.is_cuda
+                         else f"{name} must be a CUDA tensor")
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if t.dim() == 3:
-        if t.shape[0] and t.stride(2) == 1 and t.stride(1) == t.shape[2]:
-            cols = t.shape[1] * t.shape[2]
-        elif t.is_contiguous():
-            cols = t.shape[1] * t.shape[2]
-        else:
-            raise ValueError(f"the heads of a row of {name} must lie one after the other")
-    elif t.dim() == 2:
-        cols = t.shape[1]
-        if cols > 1 and t.stride(1) != 1:
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 2:
+        cols = shape[1]
+        if cols > 1 and stride[1] != 1:
             raise ValueError(f"the columns of {name} must be contiguous")
+    elif len(shape) == 3:
+        cols = shape[1] * shape[2]
+        if not t.is_contiguous() and (stride[2] != 1 or stride[1] != shape[2]):
+            raise ValueError(f"the heads of a row of {name} must lie one after the other")
     else:
         raise ValueError(f"{name} must have 2 or 3 dimensions")
     if cols != width:
         raise ValueError(f"{name} has rows of {cols}, {width} wanted")
-    if tokens is not None and t.shape[0] != tokens:
-        raise ValueError(f"{name} has {t.shape[0]} rows, {tokens} wanted")
+    if tokens is not None and shape[0] != tokens:
+        raise ValueError(f"{name} has {shape[0]} rows, {tokens} wanted")
     # a single row has no distance to the next one
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else max(width, 8)
+    return t.data_ptr(), stride[0] if shape[0] > 1 else width
 
 
 def bitnet_kv_cache_append(cache: KvCache, K: torch.Tensor, V: torch.Tensor, q_start, kv_len,
@@ -880,31 +901,30 @@ def bitnet_kv_cache_append(cache: KvCache, K: torch.Tensor, V: torch.Tensor, q_s
     """Quantise the new tokens' K and V (bf16 [tokens, kv_heads * head_dim], rows may lie apart)
     into the cache.  q_start int32 [batch + 1], kv_len int32 [batch] (with the new tokens),
     page_table int32 [batch, max_pages]."""
-    L = load_library()
-    width = cache.kv_heads * cache.head_dim
-    k, ldk = _rows(K, "K", width)
-    v, ldv = _rows(V, "V", width, K.shape[0])
-    batch = _kv_batch(cache, q_start, kv_len, page_table, K.shape[0])
-    _same_device(cache.k_codes, K, V, q_start, kv_len, page_table)
-    _rc(L.bitnet_kv_cache_append(cache._ref, ctypes.byref(batch), k, ldk, v, ldv,
-                                 _stream(stream)), "bitnet_kv_cache_append")
+    L = _lib or load_library()
+    width, dev = cache.kv_heads * cache.head_dim, cache.device
+    k, ldk = _rows(K, "K", width, None, dev)
+    tokens = K.shape[0]
+    v, ldv = _rows(V, "V", width, tokens, dev)
+    batch = _kv_batch(cache, q_start, kv_len, page_table, tokens)
+    _rc(L.bitnet_kv_cache_append(cache._ref, batch, k, ldk, v, ldv, _stream_on(stream, dev)),
+        "bitnet_kv_cache_append")
 
 
 def bitnet_kv_cache_read(cache: KvCache, tokens: int, q_start, kv_len, page_table, K=None, V=None,
                          stream=None):
     """The last q_start[s + 1] - q_start[s] tokens of each sequence as bf16, packed: returns
     (K, V), each [tokens, kv_heads * head_dim]."""
-    L = load_library()
-    width = cache.kv_heads * cache.head_dim
+    L = _lib or load_library()
+    width, dev = cache.kv_heads * cache.head_dim, cache.device
     if K is None:
         K = _empty((tokens, width), torch.bfloat16, cache.k_codes.device, stream)
     if V is None:
         V = _empty((tokens, width), torch.bfloat16, cache.k_codes.device, stream)
-    k, ldk = _rows(K, "K", width, tokens)
-    v, ldv = _rows(V, "V", width, tokens)
+    k, ldk = _rows(K, "K", width, tokens, dev)
+    v, ldv = _rows(V, "V", width, tokens, dev)
     batch = _kv_batch(cache, q_start, kv_len, page_table, tokens)
-    _same_device(cache.k_codes, K, V, q_start, kv_len, page_table)
-    _rc(L.bitnet_kv_cache_read(cache._ref, ctypes.byref(batch), k, ldk, v, ldv, _stream(stream)),
+    _rc(L.bitnet_kv_cache_read(cache._ref, batch, k, ldk, v, ldv, _stream_on(stream, dev)),
         "bitnet_kv_cache_read")
     return K, V
 
@@ -912,10 +932,16 @@ def bitnet_kv_cache_read(cache: KvCache, tokens: int, q_start, kv_len, page_tabl
 def bitnet_kv_attention_workspace_bytes(cache: KvCache, tokens: int, batch: int, max_pages: int,
                                         q_heads: int, max_new: int) -> int:
     """Bytes of workspace bitnet_kv_attention needs for such a batch (host only)."""
-    one = 16  # the query looks at sizes, not at the arrays
-    b = _CKvBatch(one, one, one, batch, max_pages, tokens)
-    return int(load_library().bitnet_kv_attention_workspace_bytes(
-        cache._ref, ctypes.byref(b), q_heads, max_new))
+    key = (tokens, batch, max_pages, q_heads, max_new)
+    need = cache._sizes.get(key)
+    if need is None:
+        one = 16  # the query looks at sizes, not at the arrays
+        b = _CKvBatch(one, one, one, batch, max_pages, tokens)
+        need = int(load_library().bitnet_kv_attention_workspace_bytes(
+            cache._ref, ctypes.byref(b), q_heads, max_new))
+        if len(cache._sizes) < 4096:
+            cache._sizes[key] = need
+    return need
 
 
 def bitnet_kv_attention(cache: KvCache, Q: torch.Tensor, q_heads: int, q_start, kv_len,
@@ -926,36 +952,37 @@ def bitnet_kv_attention(cache: KvCache, Q: torch.Tensor, q_heads: int, q_start, 
     cached states of their sequences.  max_new: the most new tokens of any sequence.  scale
     defaults to 1 / sqrt(head_dim).  Returns (Y bf16 [tokens, q_heads * head_dim], lse float
     [tokens, q_heads] or None)."""
-    L = load_library()
-    width = q_heads * cache.head_dim
-    q, ldq = _rows(Q, "Q", width)
+    L = _lib or load_library()
+    width, dev = q_heads * cache.head_dim, cache.device
+    q, ldq = _rows(Q, "Q", width, None, dev)
     tokens = Q.shape[0]
-    if Y is None:
-        Y = _empty((tokens, width), torch.bfloat16, Q.device, stream)
-    y, ldy = _rows(Y, "Y", width, tokens)
-    if lse is None:
-        if want_lse:
-            lse = _empty((tokens, q_heads), torch.float32, Q.device, stream)
-    else:
-        _check(lse, "lse", torch.float32)
-        _nbytes_at_least(lse, 4 * tokens * q_heads, "lse")
     batch = _kv_batch(cache, q_start, kv_len, page_table, tokens)
-    ref = ctypes.byref(batch)
-    if ws is None:
-        need = int(L.bitnet_kv_attention_workspace_bytes(cache._ref, ref, q_heads, max_new))
-        if need:
-            ws = _empty(need, torch.uint8, Q.device, stream)
+    if Y is None:
+        Y = (Q.new_empty((tokens, width)) if stream is None
+             else _empty((tokens, width), torch.bfloat16, Q.device, stream))
+        y, ldy = Y.data_ptr(), width
     else:
-        _check(ws, "ws")
-    _same_device(cache.k_codes, Q, Y, q_start, kv_len, page_table,
-                 *(t for t in (lse, ws) if t is not None))
-    _rc(L.bitnet_kv_attention(cache._ref, ref, q, ldq, q_heads, max_new,
-                              cache.head_dim ** -0.5 if scale is None else float(scale),
-                              int(bool(causal)), y, ldy,
-                              lse.data_ptr() if lse is not None else None,
-                              ws.data_ptr() if ws is not None else None,
-                              ws.numel() * ws.element_size() if ws is not None else 0,
-                              _stream(stream)), "bitnet_kv_attention")
+        y, ldy = _rows(Y, "Y", width, tokens, dev)
+    lse_ptr = None
+    if lse is not None:
+        lse_ptr = _plain(lse, "lse", torch.float32, None, dev)
+        _nbytes_at_least(lse, 4 * tokens * q_heads, "lse")
+    elif want_lse:
+        lse = _empty((tokens, q_heads), torch.float32, Q.device, stream)
+        lse_ptr = lse.data_ptr()
+    ws_ptr, ws_bytes = None, 0
+    if ws is not None:
+        ws_ptr, ws_bytes = _plain(ws, "ws", ws.dtype, None, dev), ws.numel() * ws.element_size()
+    else:
+        ws_bytes = bitnet_kv_attention_workspace_bytes(cache, tokens, batch.batch,
+                                                       batch.max_pages, q_heads, max_new)
+        if ws_bytes:
+            ws = _empty(ws_bytes, torch.uint8, Q.device, stream)
+            ws_ptr = ws.data_ptr()
+    _rc(L.bitnet_kv_attention(cache._ref, batch, q, ldq, q_heads, max_new,
+                              cache.head_dim ** -0.5 if scale is None else scale,
+                              1 if causal else 0, y, ldy, lse_ptr, ws_ptr, ws_bytes,
+                              _stream_on(stream, dev)), "bitnet_kv_attention")
     return Y, lse
 
 

@@ -140,6 +140,6 @@ def test_binding_refuses_what_the_library_cannot_see(B):
     with pytest.raises(ValueError, match="CUDA"):
         B.bitnet_act_quant_residual_norm(x, x, None, 1e-5, 8)
     with pytest.raises(ValueError, match="CUDA"):
-        B._rows(x, "Q", 256)
+        B._rows(x, "Q", 256, None, 0)
     with pytest.raises(TypeError):
-        B._rows([1], "Q", 256)
+        B._rows([1], "Q", 256, None, 0)
