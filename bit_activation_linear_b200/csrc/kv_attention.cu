@@ -44,8 +44,10 @@
 namespace bitnet {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 8;
 constexpr int kStages = 3;
+constexpr uint32_t kNoPage = 0xFFFFFFFFu;  // a step (a NaN that no product gives)
+constexpr float kNothing = -3.0e38f;       // the maximum of a row that has seen nothing
 constexpr int kMinChunks = 32;  // a range shorter than this does not repay the joining
 
 // The device's view of the partial sums: [2 * P][heads][rows][D] sums, then [..][rows][2] maxima
@@ -87,6 +89,18 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// Bytes 0 and 2 of four codes as fp16 numbers c * 2^-24: the byte c xor 0x80 under a zero byte is
+// the subnormal (c + 128) * 2^-24, and the subtraction is exact.
+__device__ __forceinline__ uint32_t even_codes(uint32_t w) {
+    uint32_t d;
+    asm("sub.f16x2 %0, %1, %2;" : "=r"(d) : "r"((w ^ 0x80808080u) & 0x00FF00FFu), "r"(0x00800080u));
+    return d;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
     uint32_t d;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
@@ -117,15 +131,14 @@ __device__ __forceinline__ int work_length(const KvArgs &a, const AttentionArgs 
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 3)
+__global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1)
     kv_attention_kernel(KvArgs a, AttentionArgs at, Parts parts, int P) {
     constexpr int ROWS = 8 * NT;
     constexpr int CB = kChunk * D;           // bytes of a chunk of codes
-    constexpr int STAGE = 2 * CB;            // K and V
+    constexpr int STAGE = 2 * CB + 16;       // K, V and their steps
     constexpr int KW = D / 16;               // 4-code words of a token a lane holds = k16 steps
     constexpr int MT = D / 16;               // 16-feature tiles of O^T
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float steps[kWarps][kStages][2];
     __shared__ float red_m[kWarps][ROWS], red_l[kWarps][ROWS];
     __shared__ long long scan[kWarps];
     __shared__ int found[4];
@@ -180,6 +193,13 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 3)
     if (head == 0 && tid == 0 && P > 1) parts.joins[p] = make_int4(-1, 0, 0, 0);
 
     const uint32_t ring = smem_addr(smem) + warp * kStages * STAGE;
+    // this lane's places in a stage: of the pieces it brings (and, for D = 128, four tokens on), of
+    // its first piece of K, of its pieces of V of an even and an odd token
+    const uint32_t to_even = piece<D>(lane / (D / 16), lane % (D / 16));
+    const uint32_t to_odd = piece<D>(lane / (D / 16) + 4, lane % (D / 16));
+    const uint32_t k_piece = piece<D>(n, t);
+    const uint32_t v_even = D == 128 ? piece<D>(2 * t, n) : piece<D>(2 * t, n >> 1) + (n & 1) * 8;
+    const uint32_t v_odd = D == 128 ? piece<D>(2 * t + 1, n) : piece<D>(2 * t + 1, n >> 1) + (n & 1) * 8;
     while (at_chunk < t1) {
         const KvSequence q = kv_sequence(a, s);
         const bool out_of_use = !q.valid || q.count > at.max_new;
@@ -190,9 +210,45 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 3)
         const int c1 = (int)min((long long)chunks, c0 + (t1 - at_chunk));
         const int real = length > 0 ? c1 : c0;  // an empty sequence's one chunk is not there
 
+        // ---- the ring ----
+        const int first = c0 + warp;
+        const int count = real > first ? (real - first + kWarps - 1) / kWarps : 0;
+        int page = count > 0 ? kv_page(a, s, first * kChunk) : 0;  // of the next chunk to bring in
+        int bring_pos = first * kChunk, left = count;
+        uint32_t bring_to = ring;
+        auto bring = [&]() {
+            if (left > 0) {
+                if (page >= 0) {
+                    const int64_t at_code = kv_code_at(a, page, head, bring_pos) + 16 * lane;
+                    const int8_t *ks = a.k_codes + at_code, *vs = a.v_codes + at_code;
+#pragma unroll
+                    for (int i = 0; i < CB / 512; ++i) {  // 512 bytes on: D = 128: 4 tokens, D = 64: 8
+                        const uint32_t d = bring_to + (D == 128 && (i & 1) ? to_odd : to_even) +
+                                           (D == 128 ? (i >> 1) * 1024 : i * 512);
+                        cp_async16(d, ks + 512 * i);
+                        cp_async16(d + CB, vs + 512 * i);
+                    }
+                    if (lane < 2)
+                        cp_async4(bring_to + 2 * CB + 4 * lane,
+                                  (lane ? a.v_scales : a.k_scales) +
+                                      kv_scale_at(a, page, head, bring_pos));
+                } else if (lane < 2) {
+                    // tokens of no page weigh nothing: a step of K that is marked
+                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(bring_to + 2 * CB + 4 * lane),
+                                 "r"(kNoPage) : "memory");
+                }
+                --left;
+                bring_pos += kWarps * kChunk;
+                bring_to = bring_to == ring + (kStages - 1) * STAGE ? ring : bring_to + STAGE;
+                if (left > 0) page = kv_page(a, s, bring_pos);
+            }
+            cp_async_commit();
+        };
+#pragma unroll
+        for (int k = 0; k < kStages - 1; ++k) bring();
         // ---- Q: this lane's features of row n (and n + 8), scaled to below 2 ----
         uint32_t qf[NT][2 * KW];
-        float rowf[NT][2];  // scale * log2 e / that scaling, rows 2t and 2t + 1
+        float rowf[NT][2];  // rows 2t and 2t + 1: scale * log2 e / that scaling * 2^24
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
             const int r = 8 * i + n;
@@ -224,12 +280,13 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 3)
             row_scaling(mx, down, up);
 #pragma unroll
             for (int j = 0; j < KW; ++j) {
+                // features 0 and 2, 1 and 3 of four: as even_codes takes the codes
                 qf[i][2 * j] = half2_of(__uint_as_float(w[j].x << 16) * down,
-                                        __uint_as_float(w[j].x & 0xFFFF0000u) * down);
-                qf[i][2 * j + 1] = half2_of(__uint_as_float(w[j].y << 16) * down,
+                                        __uint_as_float(w[j].y << 16) * down);
+                qf[i][2 * j + 1] = half2_of(__uint_as_float(w[j].x & 0xFFFF0000u) * down,
                                             __uint_as_float(w[j].y & 0xFFFF0000u) * down);
             }
-            const float f = up * (at.scale * kLog2e);
+            const float f = up * (at.scale * kLog2e) * 0x1p24f;
             rowf[i][0] = __shfl_sync(0xFFFFFFFFu, f, 8 * t);
             rowf[i][1] = __shfl_sync(0xFFFFFFFFu, f, 8 * t + 4);
         }
@@ -247,65 +304,34 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 3)
         float o[NT][MT][4], m[NT][2], l[NT][2];
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-            m[i][0] = m[i][1] = -INFINITY;
+            m[i][0] = m[i][1] = kNothing;
             l[i][0] = l[i][1] = 0.f;
 #pragma unroll
             for (int j = 0; j < MT; ++j) o[i][j][0] = o[i][j][1] = o[i][j][2] = o[i][j][3] = 0.f;
         }
 
-        // ---- the ring ----
-        const int first = c0 + warp;
-        const int count = real > first ? (real - first + kWarps - 1) / kWarps : 0;
-        uint32_t there = 0;  // stages whose page is valid
-        int page = count > 0 ? kv_page(a, s, first * kChunk) : 0;  // of the next chunk to bring in
-        auto bring = [&](int k) {
-            if (k < count) {
-                const int pos = (first + kWarps * k) * kChunk, st = k % kStages;
-                if (page >= 0) {
-                    const uint32_t dst = ring + st * STAGE;
-                    const int64_t at_code = kv_code_at(a, page, head, pos);
-#pragma unroll
-                    for (int i = 0; i < CB / 512; ++i) {
-                        const int x = lane + 32 * i;
-                        const uint32_t d = piece<D>(x / (D / 16), x % (D / 16));
-                        cp_async16(dst + d, a.k_codes + at_code + 16 * x);
-                        cp_async16(dst + CB + d, a.v_codes + at_code + 16 * x);
-                    }
-                    if (lane < 2)
-                        cp_async4(smem_addr(&steps[warp][st][lane]),
-                                  (lane ? a.v_scales : a.k_scales) + kv_scale_at(a, page, head, pos));
-                    there |= 1u << st;
-                } else {
-                    there &= ~(1u << st);
-                }
-                if (k + 1 < count) page = kv_page(a, s, pos + kWarps * kChunk);
-            }
-            cp_async_commit();
-        };
-#pragma unroll
-        for (int k = 0; k < kStages - 1; ++k) bring(k);
+        uint32_t stage = ring;
+        int pos = first * kChunk;
         for (int k = 0; k < count; ++k) {
-            bring(k + kStages - 1);
+            bring();
             cp_async_wait<kStages - 1>();
             __syncwarp();
-            const int st = k % kStages, pos = (first + kWarps * k) * kChunk;
-            if (there >> st & 1) {
-                const uint32_t kc = ring + st * STAGE, vc = kc + CB;
-                const float dk = steps[warp][st][0], dv = v_step(steps[warp][st][1]);
+            const uint2 step2 = lds64(stage + 2 * CB);
+            if (step2.x != kNoPage) {
+                const float dk = __uint_as_float(step2.x), dv = v_step(__uint_as_float(step2.y));
                 float sc[NT][4];
 #pragma unroll
                 for (int i = 0; i < NT; ++i) sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.f;
                 // S^T: tokens n and n + 8
 #pragma unroll
                 for (int j = 0; j < KW / 4; ++j) {
-                    const uint4 x = lds128(kc + piece<D>(n, t + 4 * j));
-                    const uint4 y = lds128(kc + piece<D>(n + 8, t + 4 * j));
+                    const uint4 x = lds128(stage + (k_piece ^ (64 * j)));
+                    const uint4 y = lds128(stage + (k_piece ^ (64 * j)) + CB / 2);
                     const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const uint32_t u = xs[e] ^ 0x80808080u, v = ys[e] ^ 0x80808080u;
-                        const uint32_t a0 = codes_lo(u), a1 = codes_lo(v), a2 = codes_hi(u),
-                                       a3 = codes_hi(v);
+                        const uint32_t a0 = even_codes(xs[e]), a1 = even_codes(ys[e]);
+                        const uint32_t a2 = even_codes(xs[e] >> 8), a3 = even_codes(ys[e] >> 8);
 #pragma unroll
                         for (int i = 0; i < NT; ++i)
                             mma_f16(sc[i], a0, a1, a2, a3, qf[i][2 * (4 * j + e)],
@@ -315,18 +341,18 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 3)
                 // V, already on its way while the weights are made
                 uint32_t vw[4][MT / 2];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int tok = 2 * t + (e & 1) + 8 * (e >> 1);
+                for (int e = 0; e < 4; ++e) {  // tokens 2t, 2t + 1, 2t + 8, 2t + 9
+                    const uint32_t from = stage + CB + (e & 1 ? v_odd : v_even) + (e >> 1) * (CB / 2);
                     if constexpr (D == 128) {
-                        const uint4 x = lds128(vc + piece<D>(tok, n));
+                        const uint4 x = lds128(from);
                         vw[e][0] = x.x; vw[e][1] = x.y; vw[e][2] = x.z; vw[e][3] = x.w;
                     } else {
-                        const uint2 x = lds64(vc + piece<D>(tok, n >> 1) + (n & 1) * 8);
+                        const uint2 x = lds64(from);
                         vw[e][0] = x.x; vw[e][1] = x.y;
                     }
                 }
                 // weights
-                const float lv = log2_approx(dv), rv = __frcp_rn(dv);
+                const float lv = log2_approx(dv), rv = rcp_approx(dv);
                 uint32_t wt[NT][2];
                 bool over = false;
 #pragma unroll
@@ -354,7 +380,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 3)
                             x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
                             x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
                             x = fmaxf(x, m[i][k2]);
-                            const float keep = m[i][k2] == -INFINITY ? 0.f : exp2_approx(m[i][k2] - x);
+                            const float keep = exp2_approx(m[i][k2] - x);
                             m[i][k2] = x;
                             l[i][k2] *= keep;
 #pragma unroll
@@ -366,10 +392,8 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 3)
                 }
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
-                    const float m0 = m[i][0] == -INFINITY ? 0.f : m[i][0];
-                    const float m1 = m[i][1] == -INFINITY ? 0.f : m[i][1];
-                    const float w0 = exp2_approx(sc[i][0] - m0), w1 = exp2_approx(sc[i][1] - m1);
-                    const float w2 = exp2_approx(sc[i][2] - m0), w3 = exp2_approx(sc[i][3] - m1);
+                    const float w0 = exp2_approx(sc[i][0] - m[i][0]), w1 = exp2_approx(sc[i][1] - m[i][1]);
+                    const float w2 = exp2_approx(sc[i][2] - m[i][0]), w3 = exp2_approx(sc[i][3] - m[i][1]);
                     const float s0 = w0 + w2, s1 = w1 + w3;
                     // a row that sees none of the chunk takes nothing of it, whatever its step is
                     if (s0 != 0.f) l[i][0] = fmaf(s0, rv, l[i][0]);
@@ -383,13 +407,12 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 3)
                     uint32_t f[2][4];  // [token pair][feature 4e ..]
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const uint32_t u = vw[2 * h][e] ^ 0x80808080u;
-                        const uint32_t v = vw[2 * h + 1][e] ^ 0x80808080u;
-                        const uint32_t x = prmt(u, v, 0x5140u), y = prmt(u, v, 0x7362u);
-                        f[h][0] = codes_lo(x);
-                        f[h][1] = codes_hi(x);
-                        f[h][2] = codes_lo(y);
-                        f[h][3] = codes_hi(y);
+                        const uint32_t x = prmt(vw[2 * h][e], vw[2 * h + 1][e], 0x5410u);
+                        const uint32_t y = prmt(vw[2 * h][e], vw[2 * h + 1][e], 0x7632u);
+                        f[h][0] = even_codes(x);
+                        f[h][1] = even_codes(x >> 8);
+                        f[h][2] = even_codes(y);
+                        f[h][3] = even_codes(y >> 8);
                     }
 #pragma unroll
                     for (int i = 0; i < NT; ++i) {
@@ -400,6 +423,8 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 3)
                 }
             }
             __syncwarp();  // the stage may be filled again
+            stage = stage == ring + (kStages - 1) * STAGE ? ring : stage + STAGE;
+            pos += kWarps * kChunk;
         }
 
         // ---- join the four warps ----
@@ -432,16 +457,15 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 3)
         const int slot = 2 * p + (at_chunk != t0);
         for (int x = tid; x < rows * (D / 4); x += 32 * kWarps) {
             const int r = x / (D / 4), d = (x - r * (D / 4)) * 4;
-            float mr = -INFINITY;
+            float mr = kNothing;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) mr = fmaxf(mr, red_m[w][r]);
             float lr = 0.f;
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                const float keep = red_m[w][r] == -INFINITY ? 0.f : exp2_approx(red_m[w][r] - mr);
+                const float keep = exp2_approx(red_m[w][r] - mr);
                 const float4 u = *reinterpret_cast<const float4 *>(acc + (w * ROWS + r) * (D + 4) + d);
-                // a warp that saw nothing has sums of 0; one whose sums are NaN keeps them
                 lr = fmaf(red_l[w][r], keep, lr);
                 v.x = fmaf(u.x, keep, v.x);
                 v.y = fmaf(u.y, keep, v.y);
@@ -449,7 +473,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 3)
                 v.w = fmaf(u.w, keep, v.w);
             }
             if (whole) {
-                const float inv = lr == 0.f ? 0.f : __fdividef(1.f, lr);
+                const float inv = lr == 0.f ? 0.f : __fdividef(0x1p24f, lr);
                 const int64_t token = q.first + r / G, qh = head * G + r % G;
                 *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(at.Y) +
                                            2 * (token * at.ldy + qh * D + d)) =
@@ -490,7 +514,7 @@ __global__ void __launch_bounds__(1024)
     for (int r0 = 0; r0 < 8 * NT; r0 += 8) {
         const int r = r0 + (warp >> 2);
         const bool live = r < rows;
-        float m = -INFINITY, l = 0.f, v[F] = {};
+        float m = kNothing, l = 0.f, v[F] = {};
         if (live) {
 #pragma unroll 4
             for (int i = quarter; i < join.y; i += 4) {
@@ -506,9 +530,7 @@ __global__ void __launch_bounds__(1024)
                     u[0] = x.x; u[1] = x.y;
                 }
                 const float mn = fmaxf(m, ml.x);
-                const float old = m == -INFINITY ? 0.f : exp2_approx(m - mn);
-                const float now = ml.x == -INFINITY ? 0.f : exp2_approx(ml.x - mn);
-                // with nothing seen the sums are 0, or NaN (which stays) where a step was
+                const float old = exp2_approx(m - mn), now = exp2_approx(ml.x - mn);
                 l = l * old + ml.y * now;
 #pragma unroll
                 for (int f = 0; f < F; ++f) v[f] = v[f] * old + u[f] * now;
@@ -528,15 +550,14 @@ __global__ void __launch_bounds__(1024)
             for (int i = 0; i < 3; ++i) {
                 const float mi = stats[warp >> 2][i][0], li = stats[warp >> 2][i][1];
                 const float mn = fmaxf(m, mi);
-                const float old = m == -INFINITY ? 0.f : exp2_approx(m - mn);
-                const float now = mi == -INFINITY ? 0.f : exp2_approx(mi - mn);
+                const float old = exp2_approx(m - mn), now = exp2_approx(mi - mn);
                 l = l * old + li * now;
 #pragma unroll
                 for (int f = 0; f < F; ++f)
                     v[f] = v[f] * old + sums[warp >> 2][i][F * lane + f] * now;
                 m = mn;
             }
-            const float inv = l == 0.f ? 0.f : __fdividef(1.f, l);
+            const float inv = l == 0.f ? 0.f : __fdividef(0x1p24f, l);
             const int64_t token = q.first + r / G, qh = head * G + r % G;
             uint8_t *Y = static_cast<uint8_t *>(at.Y) + 2 * (token * at.ldy + qh * D + F * lane);
             uint32_t y[F / 2];
@@ -563,7 +584,7 @@ int row_tiles(const KvArgs &a, const AttentionArgs &at) {
 // Blocks per key head: as many as fill the SMs, no more than the longest batch that the page table
 // allows can use.
 int worker_blocks(const KvArgs &a, int nt) {
-    const int64_t fill = kSms * (nt == 1 ? 4 : 3) / a.kv_heads;
+    const int64_t fill = kSms * (nt == 1 ? 2 : 1) / a.kv_heads;
     const int64_t most = ((int64_t)a.batch * ((int64_t)a.max_pages << a.page_shift) / kChunk +
                           a.batch + kMinChunks - 1) / kMinChunks;
     const int64_t p = fill < most ? fill : most;
@@ -578,7 +599,7 @@ template <int D, int NT>
 cudaError_t launch_decode(const KvArgs &a, const AttentionArgs &at, void *ws, cudaStream_t stream,
                           int *launches) {
     const int P = worker_blocks(a, NT);
-    constexpr int ring = kWarps * kStages * 2 * kChunk * D;
+    constexpr int ring = kWarps * kStages * (2 * kChunk * D + 16);
     constexpr int join = kWarps * 8 * NT * (D + 4) * 4;
     constexpr int smem = ring > join ? ring : join;
     Parts parts = {};

@@ -19,10 +19,40 @@
 namespace bitnet {
 namespace {
 
-// Work items are (block of a sequence that gets new tokens, state K or V, head), one warp each.
-// Sequence s owns the items from first(s) / block + 2 s on: that is non-decreasing, leaves room
-// for the blocks that n tokens can touch (n / block + 2), and needs no prefix sum.
+// A block takes a span of positions of one sequence (64 or a longer scale block where there are many,
+// else less: span_grid), for several heads, K and V: finding the sequence and its pages costs a dozen dependent loads and integer
+// divisions, which a warp a head would spend more time on than on its few KB.  Its warps go over the
+// (K or V, head) pairs, neighbours at neighbouring heads, so that together they read whole rows.
+// Sequence s owns the spans from first(s) / span + 2 s on: that is non-decreasing, leaves room for
+// the spans that n tokens can touch (n / span + 2), and needs no prefix sum.
 constexpr int kWarps = 8;
+constexpr int kSpanShift = 6;
+
+struct Span {
+    int s;            // sequence
+    KvSequence q;
+    int64_t start;    // first position, a multiple of the span
+    int lo, hi;       // the new tokens' positions in it
+};
+
+// False where this block has nothing to do.
+__device__ __forceinline__ bool find_span(const KvArgs &a, int shift, Span &x) {
+    auto begin = [&](int s) { return (int64_t)(__ldg(a.q_start + s) >> shift) + 2 * (int64_t)s; };
+    x.s = find_sequence(blockIdx.x, a.batch, begin);
+    x.q = kv_sequence(a, x.s);
+    if (!x.q.valid || x.q.count > x.q.length) {  // nothing of such a sequence is read or written
+        if (threadIdx.x == 0) record_status(a.status, BITNET_ERR_INVALID);
+        return false;
+    }
+    const int64_t j = blockIdx.x - begin(x.s);
+    if (j < 0 || x.q.count == 0) return false;
+    const int p0 = x.q.length - x.q.count;
+    x.start = ((int64_t)(p0 >> shift) + j) << shift;
+    if (x.start >= x.q.length) return false;
+    x.lo = max(p0, (int)x.start);
+    x.hi = (int)min((int64_t)x.q.length, x.start + (1 << shift));
+    return true;
+}
 
 __device__ __forceinline__ uint32_t max_bits(uint32_t m, const uint4 &v) {
     m = __vmaxu2(m, v.x & 0x7FFF7FFFu);
@@ -31,169 +61,203 @@ __device__ __forceinline__ uint32_t max_bits(uint32_t m, const uint4 &v) {
     return __vmaxu2(m, v.w & 0x7FFF7FFFu);
 }
 
-// cvt.rni saturates and turns NaN into 0
-__device__ __forceinline__ uint32_t code(float x, float s) {
-    return (uint32_t)max(min(__float2int_rn(__fmul_rn(x, s)), 127), -127) & 0xFFu;
-}
-
+// Four codes round(x * s) of two bf16 pairs: adding 1.5 * 2^23 rounds to an integer in the low byte.
+// |x| <= g gives |x * s| < 127.5, so there is nothing to clip.
 __device__ __forceinline__ uint32_t codes4(uint32_t a, uint32_t b, float s) {
-    return code(__uint_as_float(a << 16), s) | code(__uint_as_float(a & 0xFFFF0000u), s) << 8 |
-           code(__uint_as_float(b << 16), s) << 16 | code(__uint_as_float(b & 0xFFFF0000u), s) << 24;
+    const float2 magic = make_float2(12582912.f, 12582912.f);
+    // scalar products: the packed ones may be fused with the sum, which then rounds only once
+    const float2 u = __fadd2_rn(make_float2(__fmul_rn(__uint_as_float(a << 16), s),
+                                            __fmul_rn(__uint_as_float(a & 0xFFFF0000u), s)), magic);
+    const float2 v = __fadd2_rn(make_float2(__fmul_rn(__uint_as_float(b << 16), s),
+                                            __fmul_rn(__uint_as_float(b & 0xFFFF0000u), s)), magic);
+    return gather_low_bytes(__float_as_uint(u.x), __float_as_uint(u.y), __float_as_uint(v.x),
+                            __float_as_uint(v.y));
 }
 
 __device__ __forceinline__ uint32_t recode4(uint32_t c, float r) {
     uint32_t d = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) d |= code((float)(int8_t)(c >> (8 * i)), r) << (8 * i);
+    for (int i = 0; i < 4; ++i)
+        d |= ((uint32_t)__float2int_rn(__fmul_rn((float)(int8_t)(c >> (8 * i)), r)) & 0xFFu) << (8 * i);
     return d;
 }
 
-template <int D>
-__global__ void __launch_bounds__(32 * kWarps)
+// SMALL: scale blocks of 16 tokens, whose states stay in registers between the maximum and the
+// codes; longer blocks are read twice (the second time from the cache).
+template <int D, bool SMALL>
+__global__ void __launch_bounds__(32 * kWarps, 4)
     kv_append_kernel(KvArgs a, const uint8_t *__restrict__ K, int64_t ldk,
-                     const uint8_t *__restrict__ V, int64_t ldv, int64_t items) {
+                     const uint8_t *__restrict__ V, int64_t ldv, int shift) {
     constexpr int LPT = D / 8;       // lanes a token: 16 bytes of bf16 each
     constexpr int TPW = 32 / LPT;    // tokens the warp reads at once
+    constexpr int KEEP = SMALL ? 16 / TPW : 1;
     const int lane = threadIdx.x & 31;
-    const int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (item >= items) return;
-    const int per_block = 2 * a.kv_heads;
-    const int64_t w = item / per_block;
-    const int which = (int)(item - w * per_block) / a.kv_heads;
-    const int head = (int)(item - w * per_block) - which * a.kv_heads;
-    auto begin = [&](int s) {
-        return (int64_t)(__ldg(a.q_start + s) >> a.block_shift) + 2 * (int64_t)s;
-    };
-    const int s = find_sequence(w, a.batch, begin);
-    const KvSequence q = kv_sequence(a, s);
-    if (!q.valid || q.count > q.length) {  // nothing of such a sequence is written
-        if (lane == 0) record_status(a.status, BITNET_ERR_INVALID);
-        return;
-    }
-    const int block = 1 << a.block_shift, p0 = q.length - q.count;
-    const int64_t j = w - begin(s);
-    if (j < 0 || q.count == 0) return;
-    const int64_t start = ((int64_t)(p0 >> a.block_shift) + j) << a.block_shift;
-    if (start >= q.length) return;
-    const int lo = max(p0, (int)start), hi = min((int64_t)q.length, start + block);
-    const int page = kv_page(a, s, (int)start);
-    if (page < 0) return;
-    int8_t *out = (which ? a.v_codes : a.k_codes) + kv_code_at(a, page, head, (int)start);
-    float *step = (which ? a.v_scales : a.k_scales) + kv_scale_at(a, page, head, (int)start);
-    const int64_t ld = 2 * (which ? ldv : ldk);  // bytes a token row
-    const uint8_t *in = (which ? V : K) + (int64_t)(q.first + lo - p0) * ld + 2 * head * D;
-    const int sub = lane / LPT, off = lane % LPT, count = hi - lo;
-
-    uint32_t m = 0;
-    for (int t = sub; t < count; t += TPW)
-        m = max_bits(m, __ldg(reinterpret_cast<const uint4 *>(in + t * ld) + off));
-    m = __reduce_max_sync(0xFFFFFFFFu, max(m & 0xFFFFu, m >> 16));
-    float mx = __uint_as_float(m << 16);
-    if (mx < 1e-5f) mx = 1e-5f;  // keeps NaN
-    const float d_old = lo > start ? *step : 0.f;
-    const float g_old = __fmul_rn(127.f, d_old);
-    const bool grown = !(mx <= g_old) && !isnan(g_old);
-    const float g = grown ? mx : g_old;
-    const float s8 = __fdiv_rn(127.f, g);
-    if (grown && lo > start) {  // the block's older codes, with the new step
-        const float r = __fmul_rn(d_old, s8);
-        uint4 *old = reinterpret_cast<uint4 *>(out);
-        for (int i = lane; i < (lo - (int)start) * D / 16; i += 32) {
-            uint4 c = old[i];
-            c.x = recode4(c.x, r);
-            c.y = recode4(c.y, r);
-            c.z = recode4(c.z, r);
-            c.w = recode4(c.w, r);
-            old[i] = c;
+    Span x;
+    if (!find_span(a, shift, x)) return;
+    const int block = 1 << a.block_shift;
+    const int first = (x.lo - (int)x.start) >> a.block_shift;
+    const int last = (x.hi - 1 - (int)x.start) >> a.block_shift;
+    // page of block `lane` of the span (there are 1 .. 4)
+    int page = -1;
+    if (lane >= first && lane <= last) page = kv_page(a, x.s, (int)x.start + lane * block);
+    const int sub = lane / LPT, off = lane % LPT;
+    for (int pair = blockIdx.y * kWarps + (threadIdx.x >> 5); pair < 2 * a.kv_heads;
+         pair += gridDim.y * kWarps) {
+        const bool is_v = pair >= a.kv_heads;
+        const int head = is_v ? pair - a.kv_heads : pair;
+        const int64_t ld = 2 * (is_v ? ldv : ldk);  // bytes a token row
+        for (int b = first; b <= last; ++b) {
+            const int pg = __shfl_sync(0xFFFFFFFFu, page, b);
+            if (pg < 0) continue;
+            const int start = (int)x.start + b * block;
+            const int lo = max(x.lo, start), hi = min(x.hi, start + block), count = hi - lo;
+            int8_t *out = (is_v ? a.v_codes : a.k_codes) + kv_code_at(a, pg, head, start);
+            float *step = (is_v ? a.v_scales : a.k_scales) + kv_scale_at(a, pg, head, start);
+            const float d_old = lo > start ? *step : 0.f;
+            const uint8_t *in = (is_v ? V : K) +
+                                (int64_t)(x.q.first + lo - (x.q.length - x.q.count)) * ld + 2 * head * D;
+            uint4 v[KEEP];
+            uint32_t m = 0;
+            if constexpr (SMALL) {
+#pragma unroll
+                for (int i = 0; i < KEEP; ++i) {
+                    const int t = sub + i * TPW;
+                    v[i] = make_uint4(0, 0, 0, 0);
+                    if (t < count) v[i] = __ldg(reinterpret_cast<const uint4 *>(in + t * ld) + off);
+                }
+#pragma unroll
+                for (int i = 0; i < KEEP; ++i) m = max_bits(m, v[i]);
+            } else {
+#pragma unroll 4
+                for (int t = sub; t < count; t += TPW)
+                    m = max_bits(m, __ldg(reinterpret_cast<const uint4 *>(in + t * ld) + off));
+            }
+            m = __reduce_max_sync(0xFFFFFFFFu, max(m & 0xFFFFu, m >> 16));
+            float mx = __uint_as_float(m << 16);
+            if (mx < 1e-5f) mx = 1e-5f;  // keeps NaN
+            const float g_old = __fmul_rn(127.f, d_old);
+            const bool grown = !(mx <= g_old) && !isnan(g_old);
+            const float g = grown ? mx : g_old;
+            const float s8 = __fdiv_rn(127.f, g);
+            if (grown && lo > start) {  // the block's older codes, with the new step
+                const float r = __fmul_rn(d_old, s8);
+                uint4 *old = reinterpret_cast<uint4 *>(out);
+                for (int i = lane; i < (lo - start) * D / 16; i += 32) {
+                    uint4 c = old[i];
+                    c.x = recode4(c.x, r);
+                    c.y = recode4(c.y, r);
+                    c.z = recode4(c.z, r);
+                    c.w = recode4(c.w, r);
+                    old[i] = c;
+                }
+            }
+            uint2 *dst = reinterpret_cast<uint2 *>(out + (lo - start) * D);
+            if (!(g <= 3.4028235e38f)) {  // a NaN or infinite step: codes of 0, so that every
+                                          // product with it is NaN
+                for (int t = sub; t < count; t += TPW) dst[t * LPT + off] = make_uint2(0, 0);
+            } else if constexpr (SMALL) {
+#pragma unroll
+                for (int i = 0; i < KEEP; ++i) {
+                    const int t = sub + i * TPW;
+                    if (t < count)
+                        dst[t * LPT + off] = make_uint2(codes4(v[i].x, v[i].y, s8),
+                                                        codes4(v[i].z, v[i].w, s8));
+                }
+            } else {
+#pragma unroll 4
+                for (int t = sub; t < count; t += TPW) {
+                    const uint4 u = __ldg(reinterpret_cast<const uint4 *>(in + t * ld) + off);
+                    dst[t * LPT + off] = make_uint2(codes4(u.x, u.y, s8), codes4(u.z, u.w, s8));
+                }
+            }
+            __syncwarp();  // every lane has read the old step
+            if (lane == 0 && grown) *step = __fdiv_rn(g, 127.f);
         }
     }
-    uint2 *dst = reinterpret_cast<uint2 *>(out + (lo - (int)start) * D);
-    for (int t = sub; t < count; t += TPW) {
-        const uint4 x = __ldg(reinterpret_cast<const uint4 *>(in + t * ld) + off);
-        dst[t * LPT + off] = make_uint2(codes4(x.x, x.y, s8), codes4(x.z, x.w, s8));
-    }
-    __syncwarp();  // every lane has read the old step
-    if (lane == 0 && grown) *step = __fdiv_rn(g, 127.f);
 }
 
-// Reads back a sequence's last tokens, 16 positions of one head a warp.  A block is at least 16
-// tokens, so the 16 share a step.
-constexpr int kReadShift = 4;
-
+// Reads back a sequence's last tokens, 16 positions of one head at a time.  A scale block is at
+// least 16 tokens, so the 16 share a step.
 __device__ __forceinline__ uint32_t value2(uint32_t two, float d) {  // two codes -> two bf16
-    const float lo = __fmul_rn((float)(int8_t)two, d);
-    const float hi = __fmul_rn((float)(int8_t)(two >> 8), d);
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
+    return bf16x2_of(__fmul_rn((float)(int8_t)two, d), __fmul_rn((float)(int8_t)(two >> 8), d));
 }
 
 template <int D>
-__global__ void __launch_bounds__(32 * kWarps)
+__global__ void __launch_bounds__(32 * kWarps, 6)
     kv_read_kernel(KvArgs a, uint8_t *__restrict__ K, int64_t ldk, uint8_t *__restrict__ V,
-                   int64_t ldv, int64_t items) {
-    constexpr int LPT = D / 8, TPW = 32 / LPT;
+                   int64_t ldv, int shift) {
+    constexpr int LPT = D / 8, TPW = 32 / LPT, N = kChunk / TPW;
     const int lane = threadIdx.x & 31;
-    const int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (item >= items) return;
-    const int per_block = 2 * a.kv_heads;
-    const int64_t w = item / per_block;
-    const int which = (int)(item - w * per_block) / a.kv_heads;
-    const int head = (int)(item - w * per_block) - which * a.kv_heads;
-    auto begin = [&](int s) { return (int64_t)(__ldg(a.q_start + s) >> kReadShift) + 2 * (int64_t)s; };
-    const int s = find_sequence(w, a.batch, begin);
-    const KvSequence q = kv_sequence(a, s);
-    if (!q.valid || q.count > q.length) {
-        if (lane == 0) record_status(a.status, BITNET_ERR_INVALID);
-        return;
-    }
-    const int p0 = q.length - q.count;
-    const int64_t j = w - begin(s);
-    if (j < 0 || q.count == 0) return;
-    const int64_t start = ((int64_t)(p0 >> kReadShift) + j) << kReadShift;
-    if (start >= q.length) return;
-    const int lo = max(p0, (int)start), hi = min((int64_t)q.length, start + (1 << kReadShift));
-    const int page = kv_page(a, s, (int)start);
-    if (page < 0) return;
-    const uint2 *in = reinterpret_cast<const uint2 *>((which ? a.v_codes : a.k_codes) +
-                                                      kv_code_at(a, page, head, lo));
-    const float d = (which ? a.v_scales : a.k_scales)[kv_scale_at(a, page, head, (int)start)];
-    const int64_t ld = 2 * (which ? ldv : ldk);
-    uint8_t *out = (which ? V : K) + (int64_t)(q.first + lo - p0) * ld + 2 * head * D;
+    Span x;
+    if (!find_span(a, shift, x)) return;
+    const int first = (x.lo - (int)x.start) / kChunk, last = (x.hi - 1 - (int)x.start) / kChunk;
+    int page = -1;  // of chunk `lane`
+    if (lane >= first && lane <= last) page = kv_page(a, x.s, (int)x.start + lane * kChunk);
     const int sub = lane / LPT, off = lane % LPT;
-#pragma unroll 4
-    for (int t = sub; t < hi - lo; t += TPW) {
-        const uint2 c = in[t * LPT + off];
-        reinterpret_cast<uint4 *>(out + t * ld)[off] =
-            make_uint4(value2(c.x, d), value2(c.x >> 16, d), value2(c.y, d), value2(c.y >> 16, d));
+    for (int pair = blockIdx.y * kWarps + (threadIdx.x >> 5); pair < 2 * a.kv_heads;
+         pair += gridDim.y * kWarps) {
+        const bool is_v = pair >= a.kv_heads;
+        const int head = is_v ? pair - a.kv_heads : pair;
+        const int64_t ld = 2 * (is_v ? ldv : ldk);
+        for (int b = first; b <= last; ++b) {
+            const int pg = __shfl_sync(0xFFFFFFFFu, page, b);
+            if (pg < 0) continue;
+            const int start = (int)x.start + b * kChunk;
+            const uint2 *in = reinterpret_cast<const uint2 *>(
+                (is_v ? a.v_codes : a.k_codes) + kv_code_at(a, pg, head, start));
+            const float d = (is_v ? a.v_scales : a.k_scales)[kv_scale_at(a, pg, head, start)];
+            uint8_t *out = (is_v ? V : K) + 2 * head * D +
+                           (int64_t)(x.q.first + start - (x.q.length - x.q.count)) * ld;
+            uint2 c[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) c[i] = __ldcs(in + 32 * i + lane);  // within the page
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int t = sub + i * TPW;
+                if (start + t >= x.lo && start + t < x.hi)
+                    reinterpret_cast<uint4 *>(out + t * ld)[off] =
+                        make_uint4(value2(c[i].x, d), value2(c[i].x >> 16, d), value2(c[i].y, d),
+                                   value2(c[i].y >> 16, d));
+            }
+        }
     }
 }
 
 }  // namespace
 
-static int64_t kv_items(const KvArgs &a, int shift) {
-    return (((int64_t)a.tokens >> shift) + 2 * (int64_t)a.batch) * 2 * a.kv_heads;
+// The grid over spans and (K or V, head) pairs, a warp a pair: long spans where there are enough of
+// them to fill the GPU (kFill blocks), else spans of one `shortest`, and the pairs dealt to several
+// blocks.
+constexpr int kFill = 4 * kSms;
+
+static dim3 span_grid(const KvArgs &a, int shortest, int &shift) {
+    auto spans = [&](int sh) { return ((int64_t)a.tokens >> sh) + 2 * (int64_t)a.batch; };
+    shift = shortest < kSpanShift && spans(kSpanShift) < kFill ? shortest
+                                                                : max(shortest, kSpanShift);
+    const int64_t x = spans(shift), most = (2 * a.kv_heads + kWarps - 1) / kWarps;
+    const int64_t y = (kFill + x - 1) / x;
+    return dim3((unsigned)x, (unsigned)(y < most ? y : most));
 }
 
 cudaError_t launch_kv_append(const KvArgs &a, const void *K, int64_t ldk, const void *V,
                              int64_t ldv, cudaStream_t stream) {
-    const int64_t items = kv_items(a, a.block_shift);
-    const int64_t blocks = (items + kWarps - 1) / kWarps;
-    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-    auto kern = a.head_dim == 64 ? kv_append_kernel<64> : kv_append_kernel<128>;
-    kern<<<(unsigned)blocks, 32 * kWarps, 0, stream>>>(a, static_cast<const uint8_t *>(K), ldk,
-                                                       static_cast<const uint8_t *>(V), ldv, items);
+    int shift;
+    const dim3 grid = span_grid(a, a.block_shift, shift);
+    const bool small = a.block_shift == 4;
+    auto kern = a.head_dim == 64 ? (small ? kv_append_kernel<64, true> : kv_append_kernel<64, false>)
+                                 : (small ? kv_append_kernel<128, true> : kv_append_kernel<128, false>);
+    kern<<<grid, 32 * kWarps, 0, stream>>>(a, static_cast<const uint8_t *>(K), ldk,
+                                           static_cast<const uint8_t *>(V), ldv, shift);
     return cudaGetLastError();
 }
 
 cudaError_t launch_kv_read(const KvArgs &a, void *K, int64_t ldk, void *V, int64_t ldv,
                            cudaStream_t stream) {
-    const int64_t items = kv_items(a, kReadShift);
-    const int64_t blocks = (items + kWarps - 1) / kWarps;
-    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+    int shift;
+    const dim3 grid = span_grid(a, 4, shift);  // 16 tokens: what a warp takes at once
     auto kern = a.head_dim == 64 ? kv_read_kernel<64> : kv_read_kernel<128>;
-    kern<<<(unsigned)blocks, 32 * kWarps, 0, stream>>>(a, static_cast<uint8_t *>(K), ldk,
-                                                       static_cast<uint8_t *>(V), ldv, items);
+    kern<<<grid, 32 * kWarps, 0, stream>>>(a, static_cast<uint8_t *>(K), ldk,
+                                           static_cast<uint8_t *>(V), ldv, shift);
     return cudaGetLastError();
 }
 
