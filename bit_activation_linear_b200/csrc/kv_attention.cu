@@ -47,7 +47,6 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kStages = 3;
 constexpr uint32_t kNoPage = 0xFFFFFFFFu;  // a step (a NaN that no product gives)
-constexpr float kNothing = -3.0e38f;       // the maximum of a row that has seen nothing
 constexpr int kMinChunks = 32;  // a range shorter than this does not repay the joining
 
 // The device's view of the partial sums: [2 * P][heads][rows][D] sums, then [..][rows][2] maxima
@@ -98,7 +97,7 @@ __device__ __forceinline__ uint32_t even_codes(uint32_t w) {
 }
 __device__ __forceinline__ float rcp_approx(float x) {
     float y;
-    asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {

@@ -20,6 +20,8 @@
 //
 // Every wait is bounded; after a time-out (recorded) each role leaves its loop and all meet at the
 // end, where tensor memory is freed.
+#include <type_traits>
+
 #include "kv_common.cuh"
 
 namespace bitnet {
@@ -291,19 +293,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint4 kc[N], vc[N];
         float gk = 0.f, gv = 0.f;            // steps of group `lane` of warp 8
         int page = -1;                       // of group `lane` of the step to load
+        int64_t base = 0;                    // its codes
         auto pages = [&](int j) {
             const int pos = (k0 + j) * kTile + lane * kChunk;
             page = lane < kGroups && pos < q.length ? kv_page(a, s, pos) : -1;
+            base = page >= 0 ? kv_code_at(a, page, head, pos) : -1;
         };
-        auto load = [&](const int8_t *codes, uint4 (&c)[N], int j) {
+        const int in_group = (ct / PPT) % kChunk * D + ct % PPT * 16;  // the same for every piece
+        auto load = [&](const int8_t *codes, uint4 (&c)[N]) {
+            const int8_t *from = codes + in_group;
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const int token = i * TPI + ct / PPT;
-                const int pg = __shfl_sync(0xFFFFFFFFu, page, token / kChunk);
+                const int64_t at_group = __shfl_sync(0xFFFFFFFFu, base, (i * TPI + ct / PPT) / kChunk);
                 c[i] = make_uint4(0, 0, 0, 0);
-                if (pg >= 0)
-                    c[i] = ldg_nc_v4(codes + kv_code_at(a, pg, head, (k0 + j) * kTile + token) +
-                                     16 * (ct % PPT));
+                if (at_group >= 0) c[i] = ldg_nc_v4(from + at_group);
             }
         };
         auto load_steps = [&](int j) {
@@ -313,34 +316,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                 gv = v_step(__ldg(a.v_scales + at_step));
             }
         };
+        // A piece is 16 features: two 16-byte places of a row.  The lanes of the upper operand block
+        // write theirs in the other order, so that eight lanes meet in no bank.
+        const int pc = ct % PPT, row0 = ct / PPT;
+        const bool swap = pc >= 4;
+        const uint32_t to = (pc >> 2) * kBlockBytes + row0 * 128;
+        const uint32_t to_a = to + (((2 * (pc & 3) + swap) ^ (row0 & 7)) << 4), to_b = to_a ^ 16;
         auto store = [&](const uint4 (&c)[N], uint32_t stage) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int token = i * TPI + ct / PPT, pc = ct % PPT;
-                const uint32_t w[4] = {c[i].x ^ 0x80808080u, c[i].y ^ 0x80808080u,
-                                       c[i].z ^ 0x80808080u, c[i].w ^ 0x80808080u};
-                const uint4 lo = make_uint4(codes_lo(w[0]), codes_hi(w[0]), codes_lo(w[1]), codes_hi(w[1]));
-                const uint4 hi = make_uint4(codes_lo(w[2]), codes_hi(w[2]), codes_lo(w[3]), codes_hi(w[3]));
-                // 16 features = two 16-byte places of a row; the upper block's lanes write theirs in
-                // the other order, so that eight lanes meet in no bank
-                const bool swap = pc >= 4;
-                const uint32_t row = stage + (pc >> 2) * kBlockBytes + token * 128;
-                const int place = 2 * (pc & 3);
-                const uint4 f = swap ? hi : lo, g = swap ? lo : hi;
-                const uint32_t af = row + (((place + swap) ^ (token & 7)) << 4);
-                const uint32_t ag = row + (((place + !swap) ^ (token & 7)) << 4);
-                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(af), "r"(f.x), "r"(f.y),
-                             "r"(f.z), "r"(f.w) : "memory");
-                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(ag), "r"(g.x), "r"(g.y),
-                             "r"(g.z), "r"(g.w) : "memory");
+            for (int i = 0; i < N; ++i) {  // TPI tokens, a multiple of eight, further each
+                const uint32_t w0 = (swap ? c[i].z : c[i].x) ^ 0x80808080u;
+                const uint32_t w1 = (swap ? c[i].w : c[i].y) ^ 0x80808080u;
+                const uint32_t w2 = (swap ? c[i].x : c[i].z) ^ 0x80808080u;
+                const uint32_t w3 = (swap ? c[i].y : c[i].w) ^ 0x80808080u;
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(stage + to_a + i * TPI * 128),
+                             "r"(codes_lo(w0)), "r"(codes_hi(w0)), "r"(codes_lo(w1)), "r"(codes_hi(w1))
+                             : "memory");
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(stage + to_b + i * TPI * 128),
+                             "r"(codes_lo(w2)), "r"(codes_hi(w2)), "r"(codes_lo(w3)), "r"(codes_hi(w3))
+                             : "memory");
             }
             fence_proxy_async_smem();
             __syncwarp();
         };
         pages(0);
         if (ns > 0) {
-            load(a.k_codes, kc, 0);
-            load(a.v_codes, vc, 0);
+            load(a.k_codes, kc);
+            load(a.v_codes, vc);
             load_steps(0);
         }
         for (int j = 0; j < ns; ++j) {
@@ -360,14 +362,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(&sh.kfull[st]);
             if (j + 1 < ns) {
                 pages(j + 1);
-                load(a.k_codes, kc, j + 1);
+                load(a.k_codes, kc);
                 load_steps(j + 1);
             }
             if (j >= 2) ok = mbar_wait(&sh.vfree[st], ((j - 2) >> 1) & 1, a.status);
             if (!__all_sync(0xFFFFFFFFu, ok)) break;
             store(vc, sv + st * TILE_BYTES);
             if (lane == 0) mbar_arrive(&sh.vfull[st]);
-            if (j + 1 < ns) load(a.v_codes, vc, j + 1);
+            if (j + 1 < ns) load(a.v_codes, vc);
         }
     } else {
         // ---- softmax: thread = row ----
@@ -380,63 +382,64 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool live = r < rows;
         // rows that are not there see everything and are dropped
         const int seen = !live ? INT32_MAX : at.causal ? q.length - q.count + (int)(row / G) + 1 : q.length;
-        float m = -INFINITY, l = 0.f;
+        float m = kNothing, l = 0.f;
         const int ni = i ? n[1] : n[0], all_see = i ? seen_first[1] : seen_first[0];
-        for (int j = 0; j < ni; ++j) {
-            ok = mbar_wait(&sh.cfull[j & 3], (j >> 2) & 1, a.status) &&
-                 mbar_wait(&sh.sfull[i], j & 1, a.status);
-            if (!__all_sync(0xFFFFFFFFu, ok)) break;
-            tc_fence_after();
-            const float4 *group = sh.group[j & 3];
-            const int pos = (k0 + j) * kTile;
-            const bool masked = pos + kTile > all_see;
+        // one step: the row's maximum, the weights, their sum; `sees` of the 128 tokens are seen
+        auto step = [&](auto part, const float4 *group, int sees, int j) {
+            constexpr bool PART = decltype(part)::value;
             // the row's largest score * log2 e + log2 d_V
-            float top = -INFINITY;
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                uint32_t v[32];
-                tmem_ld_32x32b_x32(ts + 32 * b, v);
-                tmem_wait_ld();
-                if (masked) {
+            float top = kNothing;
+            uint32_t va[32], vb[32];
+            auto look = [&](uint32_t (&v)[32], int b) {
+                if constexpr (PART) {
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
-                        if (pos + 32 * b + e >= seen) v[e] = 0xFF800000u;
+                        if (32 * b + e >= sees) v[e] = 0xFF800000u;
                 }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const float4 g = group[2 * b + h];
                     top = fmaxf(top, fmaf(max16(v + 16 * h), rowf * g.x, g.y));
                 }
-            }
+            };
+            tmem_ld_32x32b_x32(ts, va);
+            tmem_wait_ld();
+            tmem_ld_32x32b_x32(ts + 32, vb);
+            look(va, 0);
+            tmem_wait_ld();
+            tmem_ld_32x32b_x32(ts + 64, va);
+            look(vb, 1);
+            tmem_wait_ld();
+            tmem_ld_32x32b_x32(ts + 96, vb);
+            look(va, 2);
+            tmem_wait_ld();
+            tmem_ld_32x32b_x32(ts, va);
+            look(vb, 3);
             const bool over = top > m + kSlack;
             if (__any_sync(0xFFFFFFFFu, over)) {
                 const float mn = fmaxf(m, top);
-                const float keep = m == -INFINITY ? 0.f : exp2_approx(m - mn);
+                const float keep = exp2_approx(m - mn);
                 m = mn;
                 l *= keep;
                 if (j > 0) {
-#pragma unroll
+                    tmem_wait_ld();
+#pragma unroll 1
                     for (int b = 0; b < D / 32; ++b) {
-                        uint32_t v[32];
-                        tmem_ld_32x32b_x32(to + 32 * b, v);
+                        tmem_ld_32x32b_x32(to + 32 * b, vb);
                         tmem_wait_ld();
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
-                            v[e] = __float_as_uint(__uint_as_float(v[e]) * keep);
-                        tmem_st_32x32b_x32(to + 32 * b, v);
+                            vb[e] = __float_as_uint(__uint_as_float(vb[e]) * keep);
+                        tmem_st_32x32b_x32(to + 32 * b, vb);
                     }
                 }
             }
-            const float base = m == -INFINITY ? 0.f : m;
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                uint32_t v[32], w[16];
-                tmem_ld_32x32b_x32(ts + 32 * b, v);
-                tmem_wait_ld();
+            auto weigh = [&](uint32_t (&v)[32], int b) {
+                uint32_t w[16];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const float4 g = group[2 * b + h];
-                    const float f = rowf * g.x, c = g.y - base;
+                    const float f = rowf * g.x, c = g.y - m;
                     float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
                     for (int e = 0; e < 16; e += 2) {
@@ -445,9 +448,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                         make_float2(f, f), make_float2(c, c));
                         z.x = exp2_approx(z.x);
                         z.y = exp2_approx(z.y);
-                        if (masked) {
-                            if (pos + 32 * b + 16 * h + e >= seen) z.x = 0.f;
-                            if (pos + 32 * b + 16 * h + e + 1 >= seen) z.y = 0.f;
+                        if constexpr (PART) {
+                            if (32 * b + 16 * h + e >= sees) z.x = 0.f;
+                            if (32 * b + 16 * h + e + 1 >= sees) z.y = 0.f;
                         }
                         sum = add2_rn(sum, z);
                         w[8 * h + e / 2] = half2_of(z.x, z.y);
@@ -457,7 +460,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (sg != 0.f) l = fmaf(sg, g.z, l);
                 }
                 tmem_st_32x32b_x16(ts + 16 * b, w);
-            }
+            };
+            tmem_wait_ld();
+            tmem_ld_32x32b_x32(ts + 32, vb);
+            weigh(va, 0);
+            tmem_wait_ld();
+            tmem_ld_32x32b_x32(ts + 64, va);
+            weigh(vb, 1);
+            tmem_wait_ld();
+            tmem_ld_32x32b_x32(ts + 96, vb);
+            weigh(va, 2);
+            tmem_wait_ld();
+            weigh(vb, 3);
+        };
+        for (int j = 0; j < ni; ++j) {
+            ok = mbar_wait(&sh.cfull[j & 3], (j >> 2) & 1, a.status) &&
+                 mbar_wait(&sh.sfull[i], j & 1, a.status);
+            if (!__all_sync(0xFFFFFFFFu, ok)) break;
+            tc_fence_after();
+            const float4 *group = sh.group[j & 3];
+            const int pos = (k0 + j) * kTile;
+            // a step that some row sees only in part has its own code: 128 comparisons more
+            if (pos + kTile > all_see)
+                step(std::true_type(), group, seen - pos, j);
+            else
+                step(std::false_type(), group, kTile, j);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -536,14 +563,13 @@ __global__ void __launch_bounds__(256)
     if (!q.valid || q.count > at.max_new) return;
     const int64_t row = (unit - begin(s)) * kRows + r;
     if (row < 0 || row >= (int64_t)q.count * G) return;
-    float m = -INFINITY, l = 0.f, v[F] = {};
+    float m = kNothing, l = 0.f, v[F] = {};
 #pragma unroll 4
     for (int i = 0; i < splits; ++i) {
         const int64_t piece = (uh * splits + i) * kRows + r;
         const float2 ml = *reinterpret_cast<const float2 *>(parts.stats + 2 * piece);
         const float mn = fmaxf(m, ml.x);
-        const float old = m == -INFINITY ? 0.f : exp2_approx(m - mn);
-        const float now = ml.x == -INFINITY ? 0.f : exp2_approx(ml.x - mn);
+        const float old = exp2_approx(m - mn), now = exp2_approx(ml.x - mn);
         l = l * old + ml.y * now;
 #pragma unroll
         for (int f = 0; f < F; ++f) v[f] = v[f] * old + parts.sums[piece * D + 32 * f + lane] * now;

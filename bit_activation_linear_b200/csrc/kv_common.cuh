@@ -70,6 +70,7 @@ __device__ __forceinline__ int64_t kv_scale_at(const KvArgs &a, int page, int he
 constexpr int kChunk = 16;      // tokens: a scale block is a whole number of chunks
 constexpr int kSms = 148;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kNothing = -3.0e38f;  // the maximum of a row that has seen nothing
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.f;   // log2 of how far a weight may exceed 1 before the maximum moves
 
@@ -89,12 +90,12 @@ __device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
 }
 __device__ __forceinline__ float exp2_approx(float x) {
     float y;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 __device__ __forceinline__ float log2_approx(float x) {
     float y;
-    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 
