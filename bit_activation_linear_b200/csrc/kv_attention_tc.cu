@@ -9,7 +9,7 @@
 // The two tiles alternate, so that one's softmax runs while the tensor cores work for the other.
 //
 // Warps: 0-3 and 4-7 the softmax of tile 0 and 1 (a thread owns a row: no shuffles), 8-11 turn K
-// and V codes into fp16, 12 issues the MMAs.  Codes come straight from global memory
+// codes into fp16, 12-15 V codes, 16 and 17 issue the MMAs.  Codes come straight from global memory
 // into registers one step ahead (16 bytes a load) and leave as 128-byte-swizzled fp16 rows, K as a
 // K-major operand, V (token rows, features contiguous) as an MN-major one: neither is transposed.
 //
@@ -31,8 +31,11 @@ constexpr int kTile = 128;           // rows of an MMA, and tokens of a step
 constexpr int kRows = 2 * kTile;     // rows of a block
 constexpr int kGroups = kTile / kChunk;
 constexpr int kBlockBytes = kTile * 128;  // 128 rows of 64 fp16: one swizzled operand block
-constexpr int kMmaWarp = 12;
-constexpr int kThreads = 13 * 32;
+constexpr int kMmaWarp = 16;
+constexpr int kThreads = 20 * 32;         // warps 18 and 19 only complete the last warpgroup
+// Registers: launched with 96 a thread (20 warps); 8 softmax warps take 144, the other 12 keep 64:
+// 8 * 144 + 12 * 64 = 20 * 96.
+constexpr int kManyRegisters = 144, kFewRegisters = 64;
 
 __device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                            uint32_t accumulate) {
@@ -92,21 +95,21 @@ struct Shared {
     uint32_t tmem;
 };
 
-__device__ __forceinline__ float max16(const uint32_t *v) {
-    float m = __uint_as_float(v[0]);
-#pragma unroll
-    for (int i = 1; i < kChunk; ++i) m = fmaxf(m, __uint_as_float(v[i]));
-    return m;
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 d;
-    asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
-        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
-        "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return d;
+template <int R>
+__device__ __forceinline__ void set_max_registers_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void set_max_registers_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 
 template <int D>
@@ -168,58 +171,68 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sh.kfull[i], 4);
             mbar_init(&sh.vfull[i], 4);
             mbar_init(&sh.pfull[i], 4);
-            mbar_init(&sh.kfree[i], 1);
-            mbar_init(&sh.vfree[i], 1);
+            mbar_init(&sh.kfree[i], 2);
+            mbar_init(&sh.vfree[i], 2);
             mbar_init(&sh.sfull[i], 1);
             mbar_init(&sh.ofull[i], 1);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) mbar_init(&sh.cfull[i], 1);
+        for (int i = 0; i < 4; ++i) mbar_init(&sh.cfull[i], 4);
         fence_mbar_init();
     }
     if (warp == kMmaWarp) {
         tmem_alloc(&sh.tmem, 512);
         tmem_relinquish();
     }
-    // ---- Q: a warp a row, scaled by a power of two to below 2, as fp16 ----
-    for (int r = warp; r < kRows; r += kThreads / 32) {
-        uint32_t w[D / 64];
+    // ---- Q: a warp a row (four under way), scaled by a power of two to below 2, as fp16 ----
+    constexpr int WQ = D / 64, WARPS = kThreads / 32, ROWS = 4;
+    for (int r1 = warp; r1 < kRows; r1 += ROWS * WARPS) {
+        uint32_t w[ROWS][WQ];
 #pragma unroll
-        for (int j = 0; j < D / 64; ++j) w[j] = 0;
-        if (r < rows) {
-            const int64_t row = r0 + r;
-            const uint8_t *src = static_cast<const uint8_t *>(at.Q) +
-                                 2 * ((q.first + row / G) * at.ldq +
-                                      (head * (int64_t)G + row % G) * D);
-            if constexpr (D == 128) {
-                const uint2 v = __ldg(reinterpret_cast<const uint2 *>(src) + lane);
-                w[0] = v.x;
-                w[1] = v.y;
-            } else {
-                w[0] = __ldg(reinterpret_cast<const uint32_t *>(src) + lane);
+        for (int k = 0; k < ROWS; ++k) {
+            const int r = r1 + k * WARPS;
+#pragma unroll
+            for (int j = 0; j < WQ; ++j) w[k][j] = 0;
+            if (r < rows) {
+                const int64_t row = r0 + r;
+                const uint8_t *src = static_cast<const uint8_t *>(at.Q) +
+                                     2 * ((q.first + row / G) * at.ldq +
+                                          (head * (int64_t)G + row % G) * D);
+                if constexpr (D == 128) {
+                    const uint2 v = __ldg(reinterpret_cast<const uint2 *>(src) + lane);
+                    w[k][0] = v.x;
+                    w[k][1] = v.y;
+                } else {
+                    w[k][0] = __ldg(reinterpret_cast<const uint32_t *>(src) + lane);
+                }
             }
         }
-        uint32_t mx = 0;
 #pragma unroll
-        for (int j = 0; j < D / 64; ++j) mx = __vmaxu2(mx, w[j] & 0x7FFF7FFFu);
-        mx = __reduce_max_sync(0xFFFFFFFFu, max(mx & 0xFFFFu, mx >> 16));
-        float up, down;
-        row_scaling(mx, down, up);
+        for (int k = 0; k < ROWS; ++k) {
+            const int r = r1 + k * WARPS;
+            uint32_t mx = 0;
 #pragma unroll
-        for (int j = 0; j < D / 64; ++j)
-            w[j] = half2_of(__uint_as_float(w[j] << 16) * down,
-                            __uint_as_float(w[j] & 0xFFFF0000u) * down);
-        const int i = r / kTile, rr = r % kTile;
-        uint8_t *dst = smem + i * TILE_BYTES + rr * 128;
-        if constexpr (D == 128) {  // features 4 lane ..: block lane / 16, 8 bytes
-            const int c = (lane & 15) >> 1;
-            *reinterpret_cast<uint2 *>(dst + (lane >> 4) * kBlockBytes + ((c ^ (rr & 7)) << 4) +
-                                       (lane & 1) * 8) = make_uint2(w[0], w[1]);
-        } else {  // features 2 lane ..
-            const int c = lane >> 2;
-            *reinterpret_cast<uint32_t *>(dst + ((c ^ (rr & 7)) << 4) + (lane & 3) * 4) = w[0];
+            for (int j = 0; j < WQ; ++j) mx = __vmaxu2(mx, w[k][j] & 0x7FFF7FFFu);
+            mx = __reduce_max_sync(0xFFFFFFFFu, max(mx & 0xFFFFu, mx >> 16));
+            if (r >= kRows) continue;
+            float up, down;
+            row_scaling(mx, down, up);
+#pragma unroll
+            for (int j = 0; j < WQ; ++j)
+                w[k][j] = half2_of(__uint_as_float(w[k][j] << 16) * down,
+                                   __uint_as_float(w[k][j] & 0xFFFF0000u) * down);
+            const int rr = r % kTile;
+            uint8_t *dst = smem + r / kTile * TILE_BYTES + rr * 128;
+            if constexpr (D == 128) {  // features 4 lane ..: block lane / 16, 8 bytes
+                const int c = (lane & 15) >> 1;
+                *reinterpret_cast<uint2 *>(dst + (lane >> 4) * kBlockBytes + ((c ^ (rr & 7)) << 4) +
+                                           (lane & 1) * 8) = make_uint2(w[k][0], w[k][1]);
+            } else {  // features 2 lane ..
+                const int c = lane >> 2;
+                *reinterpret_cast<uint32_t *>(dst + ((c ^ (rr & 7)) << 4) + (lane & 3) * 4) = w[k][0];
+            }
+            if (lane == 0) sh.rowf[r] = up * (at.scale * kLog2e);
         }
-        if (lane == 0) sh.rowf[r] = up * (at.scale * kLog2e);
     }
     fence_proxy_async_smem();
     tc_fence_before();
@@ -228,151 +241,154 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = sh.tmem;
     bool ok = true;
 
-    if (warp == kMmaWarp) {
-        // ---- the MMAs, one thread ----
-        if (lane == 0 && ns > 0) {
-            auto scores = [&](int i, int j) {
-                const uint32_t qa = sq + i * TILE_BYTES, kb = sk + (j & 1) * TILE_BYTES;
+    if (warp >= kMmaWarp) {
+        set_max_registers_down<kFewRegisters>();
+        // ---- the MMAs: warps 16 and 17 issue those of tile 0 and 1, one thread each ----
+        const int i = __shfl_sync(0xFFFFFFFFu, warp, 0) - kMmaWarp;
+        if (i < 2 && ns > 0) {
+            const bool leader = elect_one();
+            const int ni = i ? n[1] : n[0];
+            const uint32_t tb = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+            const uint32_t d_s = tb + i * kTile, d_o = tb + 2 * kTile + i * D;
+            const uint64_t qd = smem_desc_kmajor_sw128(sq + i * TILE_BYTES);
+            const uint64_t kd = smem_desc_kmajor_sw128(sk), vd = smem_desc_mnmajor_sw128(sv);
+            auto scores = [&](int j) {
+                const uint64_t kj = kd + (j & 1) * (TILE_BYTES >> 4);
 #pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    const uint64_t ad = smem_desc_kmajor_sw128(qa + b * kBlockBytes);
-                    const uint64_t bd = smem_desc_kmajor_sw128(kb + b * kBlockBytes);
+                for (int b = 0; b < NB; ++b)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)  // 16 features, 32 bytes, each
-                        mma_f16_ss(tmem + i * kTile, ad + 2 * e, bd + 2 * e, ID_S, b + e > 0);
-                }
+                    for (int e = 0; e < 4; ++e) {  // 16 features, 32 bytes, each
+                        const int off = b * (kBlockBytes >> 4) + 2 * e;
+                        mma_f16_ss(d_s, qd + off, kj + off, ID_S, b + e > 0);
+                    }
                 mma_commit(&sh.sfull[i]);
             };
-            auto output = [&](int i, int j) {
-                const uint64_t bd = smem_desc_mnmajor_sw128(sv + (j & 1) * TILE_BYTES);
+            auto output = [&](int j) {
+                const uint64_t vj = vd + (j & 1) * (TILE_BYTES >> 4);
 #pragma unroll
                 for (int e = 0; e < kTile / 16; ++e)  // 16 tokens: 8 columns of weights, 2 KB of V
-                    mma_f16_ts(tmem + 2 * kTile + i * D, tmem + i * kTile + 8 * e,
-                               bd + (2048 >> 4) * e, ID_O, j + e > 0);
+                    mma_f16_ts(d_o, d_s + 8 * e, vj + (2048 >> 4) * e, ID_O, j + e > 0);
             };
+            // Both warps wait for every step's K and V, also where their tile takes no part, and both
+            // release them (the barriers count two): none runs ahead of a stage's phase.
             ok = mbar_wait(&sh.kfull[0], 0, a.status);
             tc_fence_after();
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                if (ok && n[i] > 0) scores(i, 0);
-            if (ok) mma_commit(&sh.kfree[0]);
+            if (ok && leader) {
+                if (ni > 0) scores(0);
+                mma_commit(&sh.kfree[0]);
+            }
             for (int j = 0; j < ns && ok; ++j) {
                 ok = mbar_wait(&sh.vfull[j & 1], (j >> 1) & 1, a.status);
-                const bool more = j + 1 < ns;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    if (ok && j < n[i]) {
-                        ok = mbar_wait(&sh.pfull[i], j & 1, a.status);
-                        tc_fence_after();
-                        if (ok) {
-                            output(i, j);
-                            if (j == n[i] - 1) mma_commit(&sh.ofull[i]);
-                        }
-                    }
-                    if (ok && more) {
-                        if (i == 0) {
-                            ok = mbar_wait(&sh.kfull[(j + 1) & 1], ((j + 1) >> 1) & 1, a.status);
-                            tc_fence_after();
-                        }
-                        if (ok && j + 1 < n[i]) scores(i, j + 1);
-                    }
-                }
-                if (ok) {
+                if (ok && j < ni) ok = mbar_wait(&sh.pfull[i], j & 1, a.status);
+                tc_fence_after();
+                if (ok && leader) {
+                    if (j < ni) output(j);
+                    if (j == ni - 1) mma_commit(&sh.ofull[i]);
                     mma_commit(&sh.vfree[j & 1]);
-                    if (more) mma_commit(&sh.kfree[(j + 1) & 1]);
                 }
+                if (ok && j + 1 < ns) {
+                    ok = mbar_wait(&sh.kfull[(j + 1) & 1], ((j + 1) >> 1) & 1, a.status);
+                    tc_fence_after();
+                    if (ok && leader) {
+                        if (j + 1 < ni) scores(j + 1);
+                        mma_commit(&sh.kfree[(j + 1) & 1]);
+                    }
+                }
+                ok = __all_sync(0xFFFFFFFFu, ok);
             }
         }
         __syncwarp();
     } else if (warp >= 8) {
-        // ---- codes to fp16 ----
-        const int ct = tid - 8 * 32;
+        // ---- codes to fp16: a warp takes 32 tokens, two groups, of K or of V ----
+        set_max_registers_down<kFewRegisters>();
+        const bool is_k = warp < 12;
+        const int w0 = (warp & 3) * 2;       // the warp's first group
+        const int8_t *codes = is_k ? a.k_codes : a.v_codes;
+        uint64_t *full = is_k ? sh.kfull : sh.vfull, *freed = is_k ? sh.kfree : sh.vfree;
         constexpr int PPT = D / 16;          // 16-code pieces a token
-        constexpr int N = PPT;               // pieces a thread: 128 tokens * PPT / 128
-        constexpr int TPI = kTile / PPT;     // tokens the four warps cover with one piece each
-        uint4 kc[N], vc[N];
-        float gk = 0.f, gv = 0.f;            // steps of group `lane` of warp 8
-        int page = -1;                       // of group `lane` of the step to load
-        int64_t base = 0;                    // its codes
-        auto pages = [&](int j) {
-            const int pos = (k0 + j) * kTile + lane * kChunk;
-            page = lane < kGroups && pos < q.length ? kv_page(a, s, pos) : -1;
-            base = page >= 0 ? kv_code_at(a, page, head, pos) : -1;
-        };
-        const int in_group = (ct / PPT) % kChunk * D + ct % PPT * 16;  // the same for every piece
-        auto load = [&](const int8_t *codes, uint4 (&c)[N]) {
-            const int8_t *from = codes + in_group;
+        constexpr int N = PPT;               // pieces a lane: 32 tokens * PPT / 32
+        constexpr int TPI = 32 / PPT;        // tokens that the warp covers with a piece a lane
+        // This lane's piece and token of the 32 / PPT that the warp takes at once.  A piece is 16
+        // features: two 16-byte places of a swizzled row.  Eight lanes cover four pieces of one
+        // operand block in two neighbouring rows: with that they meet in no bank.
+        const int pc = D == 128 ? (lane & 3) | (lane >> 1 & 4) : lane & 3;
+        const int tok = D == 128 ? (lane >> 2 & 1) | (lane >> 3 & 2) : lane >> 2;
+        const int row0 = (warp & 3) * 32 + tok;
+        uint4 c[N];
+        float gk = 0.f, gv = 0.f;            // K warps: the steps of group w0 + lane, lane < 2
+        int entry[2] = {0, 0}, page[2] = {-1, -1};
+        // the page table is asked one step ahead of the codes
+        auto look_up = [&](int j) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int64_t at_group = __shfl_sync(0xFFFFFFFFu, base, (i * TPI + ct / PPT) / kChunk);
-                c[i] = make_uint4(0, 0, 0, 0);
-                if (at_group >= 0) c[i] = ldg_nc_v4(from + at_group);
+            for (int g = 0; g < 2; ++g) {
+                const int pos = (k0 + j) * kTile + (w0 + g) * kChunk;
+                if (pos < q.length) entry[g] = kv_page_entry(a, s, pos);
             }
         };
-        auto load_steps = [&](int j) {
-            if (warp == 8 && page >= 0) {
-                const int64_t at_step = kv_scale_at(a, page, head, (k0 + j) * kTile + lane * kChunk);
+        auto load = [&](int j) {
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                const int pos = (k0 + j) * kTile + (w0 + g) * kChunk;
+                page[g] = pos < q.length ? kv_page_checked(a, entry[g]) : -1;
+                // tokens behind the length or of an invalid page: any codes do, they weigh nothing
+                const int8_t *from = codes + (page[g] >= 0 ? kv_code_at(a, page[g], head, pos) : 0) +
+                                     tok * D + 16 * pc;
+#pragma unroll
+                for (int i = 0; i < N / 2; ++i) c[g * (N / 2) + i] = ldg_nc_v4(from + 512 * i);
+            }
+            const int mine = lane ? page[1] : page[0];
+            if (is_k && lane < 2 && mine >= 0) {
+                const int64_t at_step =
+                    kv_scale_at(a, mine, head, (k0 + j) * kTile + (w0 + lane) * kChunk);
                 gk = __ldg(a.k_scales + at_step);
-                gv = v_step(__ldg(a.v_scales + at_step));
+                gv = __ldg(a.v_scales + at_step);
             }
         };
-        // A piece is 16 features: two 16-byte places of a row.  The lanes of the upper operand block
-        // write theirs in the other order, so that eight lanes meet in no bank.
-        const int pc = ct % PPT, row0 = ct / PPT;
-        const bool swap = pc >= 4;
-        const uint32_t to = (pc >> 2) * kBlockBytes + row0 * 128;
-        const uint32_t to_a = to + (((2 * (pc & 3) + swap) ^ (row0 & 7)) << 4), to_b = to_a ^ 16;
-        auto store = [&](const uint4 (&c)[N], uint32_t stage) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) {  // TPI tokens, a multiple of eight, further each
-                const uint32_t w0 = (swap ? c[i].z : c[i].x) ^ 0x80808080u;
-                const uint32_t w1 = (swap ? c[i].w : c[i].y) ^ 0x80808080u;
-                const uint32_t w2 = (swap ? c[i].x : c[i].z) ^ 0x80808080u;
-                const uint32_t w3 = (swap ? c[i].y : c[i].w) ^ 0x80808080u;
-                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(stage + to_a + i * TPI * 128),
-                             "r"(codes_lo(w0)), "r"(codes_hi(w0)), "r"(codes_lo(w1)), "r"(codes_hi(w1))
-                             : "memory");
-                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(stage + to_b + i * TPI * 128),
-                             "r"(codes_lo(w2)), "r"(codes_hi(w2)), "r"(codes_lo(w3)), "r"(codes_hi(w3))
-                             : "memory");
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-        };
-        pages(0);
+        // With D = 128 the rows of odd pieces are 4 further than those of even ones, modulo the 8 of
+        // the swizzle.
+        const uint32_t to = (is_k ? sk : sv) + (pc >> 2) * kBlockBytes + row0 * 128 +
+                            (((2 * (pc & 3)) ^ (row0 & 7)) << 4);
         if (ns > 0) {
-            load(a.k_codes, kc);
-            load(a.v_codes, vc);
-            load_steps(0);
+            look_up(0);
+            load(0);
+            if (ns > 1) look_up(1);
         }
         for (int j = 0; j < ns; ++j) {
             const int st = j & 1;
-            if (j >= 2) ok = mbar_wait(&sh.kfree[st], ((j - 2) >> 1) & 1, a.status);
+            if (j >= 2) ok = mbar_wait(&freed[st], ((j - 2) >> 1) & 1, a.status);
             if (!__all_sync(0xFFFFFFFFu, ok)) break;
-            if (warp == 8) {
+            if (is_k) {
                 // a group behind the length or of an invalid page weighs nothing
-                if (lane < kGroups)
-                    sh.group[j & 3][lane] = page >= 0
-                                                ? make_float4(gk, log2_approx(gv), __frcp_rn(gv), 0.f)
-                                                : make_float4(0.f, -INFINITY, 0.f, 0.f);
+                if (lane < 2)
+                    sh.group[j & 3][w0 + lane] = (lane ? page[1] : page[0]) >= 0
+                                                     ? make_float4(gk, log2_approx(v_step(gv)),
+                                                                   __frcp_rn(v_step(gv)), 0.f)
+                                                     : make_float4(0.f, -INFINITY, 0.f, 0.f);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.cfull[j & 3]);
             }
-            store(kc, sk + st * TILE_BYTES);
-            if (lane == 0) mbar_arrive(&sh.kfull[st]);
-            if (j + 1 < ns) {
-                pages(j + 1);
-                load(a.k_codes, kc);
-                load_steps(j + 1);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const uint32_t x0 = c[i].x ^ 0x80808080u, x1 = c[i].y ^ 0x80808080u;
+                const uint32_t x2 = c[i].z ^ 0x80808080u, x3 = c[i].w ^ 0x80808080u;
+                const uint32_t dst = (D == 128 && (i & 1) ? to ^ 64 : to) + st * TILE_BYTES + i * TPI * 128;
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(codes_lo(x0)),
+                             "r"(codes_hi(x0)), "r"(codes_lo(x1)), "r"(codes_hi(x1)) : "memory");
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst ^ 16),
+                             "r"(codes_lo(x2)), "r"(codes_hi(x2)), "r"(codes_lo(x3)), "r"(codes_hi(x3))
+                             : "memory");
             }
-            if (j >= 2) ok = mbar_wait(&sh.vfree[st], ((j - 2) >> 1) & 1, a.status);
-            if (!__all_sync(0xFFFFFFFFu, ok)) break;
-            store(vc, sv + st * TILE_BYTES);
-            if (lane == 0) mbar_arrive(&sh.vfull[st]);
-            if (j + 1 < ns) load(a.v_codes, vc);
+            if (j + 1 < ns) {
+                load(j + 1);
+                if (j + 2 < ns) look_up(j + 2);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[st]);
         }
     } else {
         // ---- softmax: thread = row ----
+        set_max_registers_up<kManyRegisters>();
         const int i = warp >> 2;
         const int r = i * kTile + (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -384,94 +400,95 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int seen = !live ? INT32_MAX : at.causal ? q.length - q.count + (int)(row / G) + 1 : q.length;
         float m = kNothing, l = 0.f;
         const int ni = i ? n[1] : n[0], all_see = i ? seen_first[1] : seen_first[0];
-        // one step: the row's maximum, the weights, their sum; `sees` of the 128 tokens are seen
+        // One step in blocks of 32 tokens, with the maximum so far.  A weight that it makes larger than
+        // 2^12 shows in the sum of its group: no scan for the maximum is needed.  Only then (or for
+        // a row's first block) the maximum moves, the block is made again, and what the old one went
+        // into is scaled: the sum, O_i, the step's earlier weights.  `sees` of the 128 tokens are seen.
         auto step = [&](auto part, const float4 *group, int sees, int j) {
             constexpr bool PART = decltype(part)::value;
-            // the row's largest score * log2 e + log2 d_V
-            float top = kNothing;
-            uint32_t va[32], vb[32];
-            auto look = [&](uint32_t (&v)[32], int b) {
-                if constexpr (PART) {
+            auto block = [&](uint32_t (&v)[32], int b) {
+                uint32_t w[16];
+                float sg[2];
+                auto weigh = [&](float base) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (32 * b + e >= sees) v[e] = 0xFF800000u;
-                }
+                    for (int h = 0; h < 2; ++h) {
+                        const float4 g = group[2 * b + h];
+                        const float f = rowf * g.x, c = g.y - base;
+                        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float4 g = group[2 * b + h];
-                    top = fmaxf(top, fmaf(max16(v + 16 * h), rowf * g.x, g.y));
-                }
-            };
-            tmem_ld_32x32b_x32(ts, va);
-            tmem_wait_ld();
-            tmem_ld_32x32b_x32(ts + 32, vb);
-            look(va, 0);
-            tmem_wait_ld();
-            tmem_ld_32x32b_x32(ts + 64, va);
-            look(vb, 1);
-            tmem_wait_ld();
-            tmem_ld_32x32b_x32(ts + 96, vb);
-            look(va, 2);
-            tmem_wait_ld();
-            tmem_ld_32x32b_x32(ts, va);
-            look(vb, 3);
-            const bool over = top > m + kSlack;
-            if (__any_sync(0xFFFFFFFFu, over)) {
-                const float mn = fmaxf(m, top);
-                const float keep = exp2_approx(m - mn);
-                m = mn;
-                l *= keep;
-                if (j > 0) {
-                    tmem_wait_ld();
+                        for (int e = 0; e < 8; ++e) {
+                            const int k = 16 * h + 2 * e;
+                            float2 z = __ffma2_rn(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])),
+                                                  make_float2(f, f), make_float2(c, c));
+                            z.x = exp2_approx(z.x);
+                            z.y = exp2_approx(z.y);
+                            if constexpr (PART) {
+                                if (32 * b + k >= sees) z.x = 0.f;
+                                if (32 * b + k + 1 >= sees) z.y = 0.f;
+                            }
+                            sum[e & 1] = __fadd2_rn(sum[e & 1], z);
+                            w[8 * h + e] = half2_of(z.x, z.y);
+                        }
+                        sum[0] = __fadd2_rn(sum[0], sum[1]);
+                        sg[h] = sum[0].x + sum[0].y;
+                    }
+                };
+                weigh(m);
+                const bool over = fmaxf(sg[0], sg[1]) > 4096.f || m == kNothing;
+                if (__any_sync(0xFFFFFFFFu, over)) {
+                    float top = kNothing;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float4 g = group[2 * b + h];
+                        const float f = rowf * g.x;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            if (!PART || 32 * b + 16 * h + e < sees)
+                                top = fmaxf(top, fmaf(__uint_as_float(v[16 * h + e]), f, g.y));
+                    }
+                    const float mn = over ? fmaxf(m, top) : m;
+                    const float keep = exp2_approx(m - mn);
+                    m = mn;
+                    l *= keep;
+                    const uint32_t keep2 = half2_of(keep, keep);
 #pragma unroll 1
-                    for (int b = 0; b < D / 32; ++b) {
-                        tmem_ld_32x32b_x32(to + 32 * b, vb);
+                    for (int c = 0; c < b; ++c) {
+                        tmem_ld_32x32b_x16(ts + 16 * c, w);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            vb[e] = __float_as_uint(__uint_as_float(vb[e]) * keep);
-                        tmem_st_32x32b_x32(to + 32 * b, vb);
+                        for (int e = 0; e < 16; ++e)
+                            asm("mul.f16x2 %0, %0, %1;" : "+r"(w[e]) : "r"(keep2));
+                        tmem_st_32x32b_x16(ts + 16 * c, w);
                     }
-                }
-            }
-            auto weigh = [&](uint32_t (&v)[32], int b) {
-                uint32_t w[16];
+#pragma unroll 1
+                    for (int c = 0; c < (j > 0 ? D / 16 : 0); ++c) {
+                        tmem_ld_32x32b_x16(to + 16 * c, w);
+                        tmem_wait_ld();
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float4 g = group[2 * b + h];
-                    const float f = rowf * g.x, c = g.y - m;
-                    float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
-                        float2 z = fma2(make_float2(__uint_as_float(v[16 * h + e]),
-                                                    __uint_as_float(v[16 * h + e + 1])),
-                                        make_float2(f, f), make_float2(c, c));
-                        z.x = exp2_approx(z.x);
-                        z.y = exp2_approx(z.y);
-                        if constexpr (PART) {
-                            if (32 * b + 16 * h + e >= sees) z.x = 0.f;
-                            if (32 * b + 16 * h + e + 1 >= sees) z.y = 0.f;
-                        }
-                        sum = add2_rn(sum, z);
-                        w[8 * h + e / 2] = half2_of(z.x, z.y);
+                        for (int e = 0; e < 16; ++e)
+                            w[e] = __float_as_uint(__uint_as_float(w[e]) * keep);
+                        tmem_st_32x32b_x16(to + 16 * c, w);
                     }
-                    const float sg = sum.x + sum.y;
-                    // a row that sees none of the group takes nothing of it, whatever its step is
-                    if (sg != 0.f) l = fmaf(sg, g.z, l);
+                    weigh(m);
                 }
+                // a row that sees none of a group takes nothing of it, whatever its step is
+                if (sg[0] != 0.f) l = fmaf(sg[0], group[2 * b].z, l);
+                if (sg[1] != 0.f) l = fmaf(sg[1], group[2 * b + 1].z, l);
                 tmem_st_32x32b_x16(ts + 16 * b, w);
             };
+            uint32_t va[32], vb[32];
+            tmem_ld_32x32b_x32(ts, va);
             tmem_wait_ld();
             tmem_ld_32x32b_x32(ts + 32, vb);
-            weigh(va, 0);
+            block(va, 0);
             tmem_wait_ld();
             tmem_ld_32x32b_x32(ts + 64, va);
-            weigh(vb, 1);
+            block(vb, 1);
             tmem_wait_ld();
             tmem_ld_32x32b_x32(ts + 96, vb);
-            weigh(va, 2);
+            block(va, 2);
             tmem_wait_ld();
-            weigh(vb, 3);
+            block(vb, 3);
         };
         for (int j = 0; j < ni; ++j) {
             ok = mbar_wait(&sh.cfull[j & 3], (j >> 2) & 1, a.status) &&

@@ -42,14 +42,20 @@ __device__ __forceinline__ KvSequence kv_sequence(const KvArgs &a, int s) {
     return q;
 }
 
-// Page that holds `position` of sequence s, or -1 (recorded as an invalid argument).
-__device__ __forceinline__ int kv_page(const KvArgs &a, int s, int position) {
-    const int page = __ldg(a.page_table + (int64_t)s * a.max_pages + (position >> a.page_shift));
+// Page that holds `position` of sequence s, or -1 (recorded as an invalid argument); the entry of
+// the page table and its check apart, for kernels that ask for it ahead of its use.
+__device__ __forceinline__ int kv_page_entry(const KvArgs &a, int s, int position) {
+    return __ldg(a.page_table + (int64_t)s * a.max_pages + (position >> a.page_shift));
+}
+__device__ __forceinline__ int kv_page_checked(const KvArgs &a, int page) {
     if (page < 0 || page >= a.num_pages) {
         record_status(a.status, BITNET_ERR_INVALID);
         return -1;
     }
     return page;
+}
+__device__ __forceinline__ int kv_page(const KvArgs &a, int s, int position) {
+    return kv_page_checked(a, kv_page_entry(a, s, position));
 }
 
 // Codes of a position in a page, and the step of its block.
