@@ -89,7 +89,7 @@ struct TcParts {
 };
 
 struct Shared {
-    uint64_t kfull[2], kfree[2], vfull[2], vfree[2], sfull[2], pfull[2], ofull[2], cfull[4];
+    uint64_t kfull[2], kfree[2], vfull[2], vfree[2], sfull[2], pfull[2], ofull[2], half[2], cfull[4];
     float4 group[4][kGroups];  // {d_K, log2 d_V, 1 / d_V} of the 16-token groups of a step
     float rowf[kRows];
     uint32_t tmem;
@@ -144,6 +144,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tile < 0 || tile * kRows >= all_rows) return;
     const int64_t r0 = tile * kRows;
     const int rows = (int)min((int64_t)kRows, all_rows - r0);
+    // row r of this block is row (rem + r) % G of token base + (rem + r) / G
+    const int base = (int)(r0 / G), rem = (int)(r0 - (int64_t)base * G);
+    auto token_of = [&](int r) { return base + (rem + r) / G; };
+    auto member_of = [&](int r) { return (rem + r) % G; };
     // tokens that the last row of tile i sees, and the steps that it takes
     int n[2], seen_first[2];
     int steps = 0;
@@ -152,9 +156,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         int sees = 0;
         seen_first[i] = 0;
         if (rows > i * kTile) {
-            const int64_t last = r0 + min(rows, (i + 1) * kTile) - 1, first = r0 + i * kTile;
-            sees = at.causal ? q.length - q.count + (int)(last / G) + 1 : q.length;
-            seen_first[i] = at.causal ? q.length - q.count + (int)(first / G) + 1 : q.length;
+            sees = at.causal ? q.length - q.count + token_of(min(rows, (i + 1) * kTile) - 1) + 1 : q.length;
+            seen_first[i] = at.causal ? q.length - q.count + token_of(i * kTile) + 1 : q.length;
         }
         n[i] = sees > 0 ? (sees + kTile - 1) / kTile : 0;
         steps = max(steps, n[i]);
@@ -171,6 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sh.kfull[i], 4);
             mbar_init(&sh.vfull[i], 4);
             mbar_init(&sh.pfull[i], 4);
+            mbar_init(&sh.half[i], 4);
             mbar_init(&sh.kfree[i], 2);
             mbar_init(&sh.vfree[i], 2);
             mbar_init(&sh.sfull[i], 1);
@@ -186,6 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // ---- Q: a warp a row (four under way), scaled by a power of two to below 2, as fp16 ----
     constexpr int WQ = D / 64, WARPS = kThreads / 32, ROWS = 4;
+#pragma unroll 1
     for (int r1 = warp; r1 < kRows; r1 += ROWS * WARPS) {
         uint32_t w[ROWS][WQ];
 #pragma unroll
@@ -194,10 +199,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < WQ; ++j) w[k][j] = 0;
             if (r < rows) {
-                const int64_t row = r0 + r;
                 const uint8_t *src = static_cast<const uint8_t *>(at.Q) +
-                                     2 * ((q.first + row / G) * at.ldq +
-                                          (head * (int64_t)G + row % G) * D);
+                                     2 * ((int64_t)(q.first + token_of(r)) * at.ldq +
+                                          (int64_t)(head * G + member_of(r)) * D);
                 if constexpr (D == 128) {
                     const uint2 v = __ldg(reinterpret_cast<const uint2 *>(src) + lane);
                     w[k][0] = v.x;
@@ -394,37 +398,42 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + i * kTile + lanes, to = tmem + 2 * kTile + i * D + lanes;
         const float rowf = sh.rowf[r];
-        const int64_t row = r0 + r;
         const bool live = r < rows;
         // rows that are not there see everything and are dropped
-        const int seen = !live ? INT32_MAX : at.causal ? q.length - q.count + (int)(row / G) + 1 : q.length;
+        const int seen = !live ? INT32_MAX : at.causal ? q.length - q.count + token_of(r) + 1 : q.length;
         float m = kNothing, l = 0.f;
         const int ni = i ? n[1] : n[0], all_see = i ? seen_first[1] : seen_first[0];
         // One step in blocks of 32 tokens, with the maximum so far.  A weight that it makes larger than
         // 2^12 shows in the sum of its group: no scan for the maximum is needed.  Only then (or for
         // a row's first block) the maximum moves, the block is made again, and what the old one went
         // into is scaled: the sum, O_i, the step's earlier weights.  `sees` of the 128 tokens are seen.
+        // The code is kept short (loops, one copy of the block): unrolled it was 110 KB, and fetching
+        // instructions bound the kernel.
         auto step = [&](auto part, const float4 *group, int sees, int j) {
             constexpr bool PART = decltype(part)::value;
             auto block = [&](uint32_t (&v)[32], int b) {
                 uint32_t w[16];
+                const float4 g0 = group[2 * b], g1 = group[2 * b + 1];
+                const float f[2] = {rowf * g0.x, rowf * g1.x};
+                const int left = sees - 32 * b;
                 float sg[2];
-                auto weigh = [&](float base) {
+                bool moved = false;
+#pragma unroll 1
+                for (;;) {
+                    const float c[2] = {g0.y - m, g1.y - m};
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const float4 g = group[2 * b + h];
-                        const float f = rowf * g.x, c = g.y - base;
                         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
                             const int k = 16 * h + 2 * e;
                             float2 z = __ffma2_rn(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])),
-                                                  make_float2(f, f), make_float2(c, c));
+                                                  make_float2(f[h], f[h]), make_float2(c[h], c[h]));
                             z.x = exp2_approx(z.x);
                             z.y = exp2_approx(z.y);
                             if constexpr (PART) {
-                                if (32 * b + k >= sees) z.x = 0.f;
-                                if (32 * b + k + 1 >= sees) z.y = 0.f;
+                                if (k >= left) z.x = 0.f;
+                                if (k + 1 >= left) z.y = 0.f;
                             }
                             sum[e & 1] = __fadd2_rn(sum[e & 1], z);
                             w[8 * h + e] = half2_of(z.x, z.y);
@@ -432,67 +441,66 @@ __global__ void __launch_bounds__(kThreads, 1)
                         sum[0] = __fadd2_rn(sum[0], sum[1]);
                         sg[h] = sum[0].x + sum[0].y;
                     }
-                };
-                weigh(m);
-                const bool over = fmaxf(sg[0], sg[1]) > 4096.f || m == kNothing;
-                if (__any_sync(0xFFFFFFFFu, over)) {
+                    const bool over = fmaxf(sg[0], sg[1]) > 4096.f || m == kNothing;
+                    if (moved || !__any_sync(0xFFFFFFFFu, over)) break;
+                    moved = true;
                     float top = kNothing;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const float4 g = group[2 * b + h];
-                        const float f = rowf * g.x;
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            if (!PART || 32 * b + 16 * h + e < sees)
-                                top = fmaxf(top, fmaf(__uint_as_float(v[16 * h + e]), f, g.y));
-                    }
+                    for (int e = 0; e < 32; ++e)
+                        if (!PART || e < left)
+                            top = fmaxf(top, fmaf(__uint_as_float(v[e]), f[e / 16], e < 16 ? g0.y : g1.y));
                     const float mn = over ? fmaxf(m, top) : m;
                     const float keep = exp2_approx(m - mn);
                     m = mn;
                     l *= keep;
                     const uint32_t keep2 = half2_of(keep, keep);
 #pragma unroll 1
-                    for (int c = 0; c < b; ++c) {
-                        tmem_ld_32x32b_x16(ts + 16 * c, w);
+                    for (int c16 = 0; c16 < b; ++c16) {
+                        tmem_ld_32x32b_x16(ts + 16 * c16, w);
                         tmem_wait_ld();
 #pragma unroll
                         for (int e = 0; e < 16; ++e)
                             asm("mul.f16x2 %0, %0, %1;" : "+r"(w[e]) : "r"(keep2));
-                        tmem_st_32x32b_x16(ts + 16 * c, w);
+                        tmem_st_32x32b_x16(ts + 16 * c16, w);
                     }
 #pragma unroll 1
-                    for (int c = 0; c < (j > 0 ? D / 16 : 0); ++c) {
-                        tmem_ld_32x32b_x16(to + 16 * c, w);
+                    for (int c16 = 0; c16 < (j > 0 ? D / 16 : 0); ++c16) {
+                        tmem_ld_32x32b_x16(to + 16 * c16, w);
                         tmem_wait_ld();
 #pragma unroll
                         for (int e = 0; e < 16; ++e)
                             w[e] = __float_as_uint(__uint_as_float(w[e]) * keep);
-                        tmem_st_32x32b_x16(to + 16 * c, w);
+                        tmem_st_32x32b_x16(to + 16 * c16, w);
                     }
-                    weigh(m);
                 }
                 // a row that sees none of a group takes nothing of it, whatever its step is
-                if (sg[0] != 0.f) l = fmaf(sg[0], group[2 * b].z, l);
-                if (sg[1] != 0.f) l = fmaf(sg[1], group[2 * b + 1].z, l);
+                if (sg[0] != 0.f) l = fmaf(sg[0], g0.z, l);
+                if (sg[1] != 0.f) l = fmaf(sg[1], g1.z, l);
                 tmem_st_32x32b_x16(ts + 16 * b, w);
             };
             uint32_t va[32], vb[32];
             tmem_ld_32x32b_x32(ts, va);
-            tmem_wait_ld();
-            tmem_ld_32x32b_x32(ts + 32, vb);
-            block(va, 0);
-            tmem_wait_ld();
-            tmem_ld_32x32b_x32(ts + 64, va);
-            block(vb, 1);
-            tmem_wait_ld();
-            tmem_ld_32x32b_x32(ts + 96, vb);
-            block(va, 2);
-            tmem_wait_ld();
-            block(vb, 3);
+#pragma unroll 1
+            for (int b = 0; b < 4; b += 2) {  // the next block's scores are under way
+                tmem_wait_ld();
+                tmem_ld_32x32b_x32(ts + 32 * b + 32, vb);
+                block(va, b);
+                tmem_wait_ld();
+                if (b == 0) tmem_ld_32x32b_x32(ts + 64, va);
+                block(vb, b + 1);
+                if (b == 0) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.half[i]);
+                }
+            }
         };
         for (int j = 0; j < ni; ++j) {
             ok = mbar_wait(&sh.cfull[j & 3], (j >> 2) & 1, a.status) &&
                  mbar_wait(&sh.sfull[i], j & 1, a.status);
+            // Half a step apart: a tile begins when the other one is half through, so that the MMAs of
+            // one run under the softmax of the other instead of both waiting at the same time.
+            if (i == 1 && j < n[0]) ok = ok && mbar_wait(&sh.half[0], j & 1, a.status);
+            if (i == 0 && j > 0 && j <= n[1]) ok = ok && mbar_wait(&sh.half[1], (j - 1) & 1, a.status);
             if (!__all_sync(0xFFFFFFFFu, ok)) break;
             tc_fence_after();
             const float4 *group = sh.group[j & 3];
@@ -511,11 +519,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ni > 0 && ok) ok = mbar_wait(&sh.ofull[i], 0, a.status);
         ok = __all_sync(0xFFFFFFFFu, ok);
         tc_fence_after();
-        const int64_t token = q.first + row / G, qh = head * (int64_t)G + row % G;
+        const int64_t token = q.first + token_of(r), qh = head * G + member_of(r);
         const float inv = l == 0.f ? 0.f : __fdividef(1.f, l);
         const int64_t piece = (((int64_t)unit * a.kv_heads + head) * splits + split) * kRows + r;
         if (ok) {
-#pragma unroll
+#pragma unroll 1
             for (int b = 0; b < D / 32; ++b) {
                 uint32_t v[32];
                 if (ni > 0) {
