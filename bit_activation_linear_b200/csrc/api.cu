@@ -829,6 +829,11 @@ int attention_args(const KvArgs &a, int64_t q_heads, int64_t max_new, AttentionA
                     a.kv_heads);
     if (max_new < 1 || max_new > (1 << 28))
         return fail(BITNET_ERR_INVALID, "max_new = %lld must be in 1 .. 2^28", (long long)max_new);
+    // blocks of the prompts' kernel: 256 rows of a key head each, and one more a sequence
+    const int64_t units = (a.tokens * (q_heads / a.kv_heads) >> 8) + a.batch;
+    if (units * a.kv_heads > INT32_MAX / 64)
+        return fail(BITNET_ERR_UNSUPPORTED, "%lld tokens of %lld heads are too many for one call",
+                    (long long)a.tokens, (long long)q_heads);
     at->q_heads = (int)q_heads;
     at->max_new = (int)max_new;
     return BITNET_OK;

@@ -88,13 +88,6 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// Bytes 0 and 2 of four codes as fp16 numbers c * 2^-24: the byte c xor 0x80 under a zero byte is
-// the subnormal (c + 128) * 2^-24, and the subtraction is exact.
-__device__ __forceinline__ uint32_t even_codes(uint32_t w) {
-    uint32_t d;
-    asm("sub.f16x2 %0, %1, %2;" : "=r"(d) : "r"((w ^ 0x80808080u) & 0x00FF00FFu), "r"(0x00800080u));
-    return d;
-}
 __device__ __forceinline__ float rcp_approx(float x) {
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -192,6 +185,8 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1)
     if (head == 0 && tid == 0 && P > 1) parts.joins[p] = make_int4(-1, 0, 0, 0);
 
     const uint32_t ring = smem_addr(smem) + warp * kStages * STAGE;
+    const int code_shift = a.page_shift + (D == 128 ? 7 : 6), scale_shift = a.page_shift - a.block_shift;
+    const float *my_scales = lane ? a.v_scales : a.k_scales;
     // this lane's places in a stage: of the pieces it brings (and, for D = 128, four tokens on), of
     // its first piece of K, of its pieces of V of an even and an odd token
     const uint32_t to_even = piece<D>(lane / (D / 16), lane % (D / 16));
@@ -212,13 +207,16 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1)
         // ---- the ring ----
         const int first = c0 + warp;
         const int count = real > first ? (real - first + kWarps - 1) / kWarps : 0;
-        int page = count > 0 ? kv_page(a, s, first * kChunk) : 0;  // of the next chunk to bring in
-        int bring_pos = first * kChunk, left = count;
+        const int32_t *table = a.page_table + (int64_t)s * a.max_pages;
+        int page = count > 0 ? __ldg(table + (first * kChunk >> a.page_shift)) : 0;  // of the next
+        int bring_pos = first * kChunk, left = count;                                 // chunk
         uint32_t bring_to = ring;
         auto bring = [&]() {
             if (left > 0) {
-                if (page >= 0) {
-                    const int64_t at_code = kv_code_at(a, page, head, bring_pos) + 16 * lane;
+                if ((uint32_t)page < (uint32_t)a.num_pages) {
+                    const int in_page = bring_pos & ((1 << a.page_shift) - 1);
+                    const int64_t tile = (int64_t)page * a.kv_heads + head;
+                    const int64_t at_code = (tile << code_shift) + (in_page * D + 16 * lane);
                     const int8_t *ks = a.k_codes + at_code, *vs = a.v_codes + at_code;
 #pragma unroll
                     for (int i = 0; i < CB / 512; ++i) {  // 512 bytes on: D = 128: 4 tokens, D = 64: 8
@@ -229,17 +227,18 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1)
                     }
                     if (lane < 2)
                         cp_async4(bring_to + 2 * CB + 4 * lane,
-                                  (lane ? a.v_scales : a.k_scales) +
-                                      kv_scale_at(a, page, head, bring_pos));
-                } else if (lane < 2) {
+                                  my_scales + (tile << scale_shift) + (in_page >> a.block_shift));
+                } else {
                     // tokens of no page weigh nothing: a step of K that is marked
-                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(bring_to + 2 * CB + 4 * lane),
-                                 "r"(kNoPage) : "memory");
+                    record_status(a.status, BITNET_ERR_INVALID);
+                    if (lane < 2)
+                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(bring_to + 2 * CB + 4 * lane),
+                                     "r"(kNoPage) : "memory");
                 }
                 --left;
                 bring_pos += kWarps * kChunk;
                 bring_to = bring_to == ring + (kStages - 1) * STAGE ? ring : bring_to + STAGE;
-                if (left > 0) page = kv_page(a, s, bring_pos);
+                if (left > 0) page = __ldg(table + (bring_pos >> a.page_shift));
             }
             cp_async_commit();
         };
@@ -247,7 +246,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1)
         for (int k = 0; k < kStages - 1; ++k) bring();
         // ---- Q: this lane's features of row n (and n + 8), scaled to below 2 ----
         uint32_t qf[NT][2 * KW];
-        float rowf[NT][2];  // rows 2t and 2t + 1: scale * log2 e / that scaling * 2^24
+        float rowf[NT][2];  // scale * log2 e / that scaling, rows 2t and 2t + 1
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
             const int r = 8 * i + n;
@@ -279,13 +278,12 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1)
             row_scaling(mx, down, up);
 #pragma unroll
             for (int j = 0; j < KW; ++j) {
-                // features 0 and 2, 1 and 3 of four: as even_codes takes the codes
                 qf[i][2 * j] = half2_of(__uint_as_float(w[j].x << 16) * down,
-                                        __uint_as_float(w[j].y << 16) * down);
-                qf[i][2 * j + 1] = half2_of(__uint_as_float(w[j].x & 0xFFFF0000u) * down,
+                                        __uint_as_float(w[j].x & 0xFFFF0000u) * down);
+                qf[i][2 * j + 1] = half2_of(__uint_as_float(w[j].y << 16) * down,
                                             __uint_as_float(w[j].y & 0xFFFF0000u) * down);
             }
-            const float f = up * (at.scale * kLog2e) * 0x1p24f;
+            const float f = up * (at.scale * kLog2e);
             rowf[i][0] = __shfl_sync(0xFFFFFFFFu, f, 8 * t);
             rowf[i][1] = __shfl_sync(0xFFFFFFFFu, f, 8 * t + 4);
         }
@@ -329,8 +327,9 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1)
                     const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const uint32_t a0 = even_codes(xs[e]), a1 = even_codes(ys[e]);
-                        const uint32_t a2 = even_codes(xs[e] >> 8), a3 = even_codes(ys[e] >> 8);
+                        const uint32_t u = xs[e] ^ 0x80808080u, v = ys[e] ^ 0x80808080u;
+                        const uint32_t a0 = codes_lo(u), a1 = codes_lo(v), a2 = codes_hi(u),
+                                       a3 = codes_hi(v);
 #pragma unroll
                         for (int i = 0; i < NT; ++i)
                             mma_f16(sc[i], a0, a1, a2, a3, qf[i][2 * (4 * j + e)],
@@ -406,12 +405,13 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1)
                     uint32_t f[2][4];  // [token pair][feature 4e ..]
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const uint32_t x = prmt(vw[2 * h][e], vw[2 * h + 1][e], 0x5410u);
-                        const uint32_t y = prmt(vw[2 * h][e], vw[2 * h + 1][e], 0x7632u);
-                        f[h][0] = even_codes(x);
-                        f[h][1] = even_codes(x >> 8);
-                        f[h][2] = even_codes(y);
-                        f[h][3] = even_codes(y >> 8);
+                        const uint32_t u = vw[2 * h][e] ^ 0x80808080u;
+                        const uint32_t v = vw[2 * h + 1][e] ^ 0x80808080u;
+                        const uint32_t x = prmt(u, v, 0x5140u), y = prmt(u, v, 0x7362u);
+                        f[h][0] = codes_lo(x);
+                        f[h][1] = codes_hi(x);
+                        f[h][2] = codes_lo(y);
+                        f[h][3] = codes_hi(y);
                     }
 #pragma unroll
                     for (int i = 0; i < NT; ++i) {
@@ -472,7 +472,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1)
                 v.w = fmaf(u.w, keep, v.w);
             }
             if (whole) {
-                const float inv = lr == 0.f ? 0.f : __fdividef(0x1p24f, lr);
+                const float inv = lr == 0.f ? 0.f : __fdividef(1.f, lr);
                 const int64_t token = q.first + r / G, qh = head * G + r % G;
                 *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(at.Y) +
                                            2 * (token * at.ldy + qh * D + d)) =
@@ -556,7 +556,7 @@ __global__ void __launch_bounds__(1024)
                     v[f] = v[f] * old + sums[warp >> 2][i][F * lane + f] * now;
                 m = mn;
             }
-            const float inv = l == 0.f ? 0.f : __fdividef(0x1p24f, l);
+            const float inv = l == 0.f ? 0.f : __fdividef(1.f, l);
             const int64_t token = q.first + r / G, qh = head * G + r % G;
             uint8_t *Y = static_cast<uint8_t *>(at.Y) + 2 * (token * at.ldy + qh * D + F * lane);
             uint32_t y[F / 2];

@@ -91,6 +91,12 @@ def test_matrices_that_are_refused(B, lib):
         assert attend(lib, cache(B), batch(B), **bad) == -1, bad
 
 
+def test_more_rows_than_a_launch_holds_are_refused(B, lib):
+    big = batch(B, tokens=2**28)
+    assert attend(lib, cache(B, kv_heads=1024), big, heads=128 * 1024, ldq=2**24, ldy=2**24) == -2
+    assert lib.bitnet_kv_attention_workspace_bytes(cache(B, kv_heads=1024), big, 128 * 1024, 1) == 0
+
+
 def test_empty_calls_are_answered_without_a_device(B, lib):
     for change in (dict(tokens=0), dict(batch=0, q_start=None, kv_len=None, page_table=None)):
         for call in (append, read, attend):

@@ -480,6 +480,80 @@ def test_attention_strided_rows_and_hints(B):
         assert np.all(np.abs(o - y) <= BF16_HALF * np.abs(y) + tol_y * (1 + BF16_HALF))
 
 
+def test_offsets_beyond_32_bits(B):
+    """Pages whose codes lie more than 2^31 and 2^32 bytes into the cache give what the same pages
+    give in a small one: writing, reading back and both attention kernels."""
+    rng = np.random.default_rng(17)
+    heads, dim, page, block, q_heads = 2, 128, 256, 16, 4
+    tile = heads * page * dim
+    places = [3, 2**31 // tile + 1, 2**32 // tile + 2]          # positions 0.., 256.., 512..
+    pages = places[-1] + 2
+    big = B.KvCache.empty(pages, heads, dim, page, block)
+    small = B.KvCache.empty(4, heads, dim, page, block)
+    length = 600
+    states = [bf16(rng.standard_normal((length, heads * dim)))[0] for _ in range(2)]
+    tables = {big: ints([places]), small: ints([[2, 0, 3]])}
+    results = []
+    for cache in (big, small):
+        table = tables[cache]
+        B.bitnet_kv_cache_append(cache, states[0][:599], states[1][:599], ints([0, 599]),
+                                 ints([599]), table)
+        B.bitnet_kv_cache_append(cache, states[0][599:], states[1][599:], ints([0, 1]),
+                                 ints([600]), table)
+        out = list(B.bitnet_kv_cache_read(cache, 600, ints([0, 600]), ints([600]), table))
+        for new in (1, 50):
+            Q = torch.from_numpy(np.random.default_rng(new).standard_normal(
+                (new, q_heads * dim)).astype(np.float32)).bfloat16().cuda()
+            out += B.bitnet_kv_attention(cache, Q, q_heads, ints([0, new]), ints([600]), table, new,
+                                         want_lse=True)
+        results.append(out)
+    B.bitnet_sync_status()
+    assert all(torch.equal(x, y) for x, y in zip(*results))
+
+
+@pytest.mark.parametrize("batch", [130, 1100])
+def test_many_sequences(B, batch):
+    """More sequences than a block has threads, most of them short or empty, in every call."""
+    rng = np.random.default_rng(batch)
+    heads, dim, page = 1, 64, 16
+    lengths = [int(x) for x in rng.integers(0, 40, batch)]
+    new = [min(n, int(rng.integers(0, 3))) for n in lengths]
+    b, cache, got = filled(B, rng, lengths, new, heads, dim, page, 16, gap=1, behind=2)
+    check_attention(B, b, cache, got, 2, max_new=2)
+    check_attention(B, b, cache, got, 2, max_new=40)
+    shape = (b.tokens, heads, dim)
+    K, k = bf16(rng.standard_normal(shape) * 3)
+    V, v = bf16(rng.standard_normal(shape) * 3)
+    cache.append((k, v), b.q_start, b.kv_len, b.table)
+    B.bitnet_kv_cache_append(got, K, V, *b.device())
+    B.bitnet_sync_status()
+    same_cache(got, cache)
+
+
+def test_attention_scores_that_keep_growing_and_falling(B):
+    """The maximum moves in every chunk, or never again after the first one: rising and falling
+    keys, by steps below and above what moves it, for both kernels."""
+    for new in (1, 40):
+        for slope in (0.9, -0.9, 0.05, -0.05):
+            rng = np.random.default_rng(3)
+            heads, dim, page, length = 1, 64, 32, 700
+            b = Batch([length], [new], page, rng)
+            cache = ref.Cache(b.pages, heads, dim, page, 16, rng)
+            k = rng.standard_normal((length, heads, dim)).astype(np.float32) * 0.1
+            k[:, 0, 0] = slope * np.arange(length)
+            v = rng.standard_normal((length, heads, dim)).astype(np.float32)
+            cache.append((bf16(k)[1], bf16(v)[1]), [0, length], [length], b.table)
+            got = to_device(B, cache)
+            Q, q = bf16(np.abs(rng.standard_normal((b.tokens, 2 * dim))) + 0.5)
+            Y, lse = B.bitnet_kv_attention(got, Q, 2, *b.device(), new, want_lse=True)
+            B.bitnet_sync_status()
+            y, l, tol_y, tol_l = ref.attention(cache, q.astype(np.float64).reshape(-1, 2, dim),
+                                               b.q_start, b.kv_len, b.table, dim ** -0.5, True)
+            got_y = Y.float().cpu().numpy().reshape(y.shape)
+            assert np.all(np.abs(got_y - y) <= BF16_HALF * np.abs(y) + tol_y * (1 + BF16_HALF))
+            assert np.all(np.abs(lse.cpu().numpy() - l) <= tol_l)
+
+
 # ----------------------------------------------------------------------------------------
 # what the device finds wrong; streams and graphs
 # ----------------------------------------------------------------------------------------
