@@ -497,12 +497,15 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1)
 }
 
 // Joins the pieces of the sequence that begins in the range of block p and ends in a later one:
-// eight rows of one key head, four warps each, the pieces in turn.
+// four rows of one key head at a time, four warps each, the pieces in turn.  (Most blocks have
+// nothing to join; with eight rows at a time starting them took 2 us more.)
+constexpr int kJoinRows = 4;
+
 template <int D, int NT>
-__global__ void __launch_bounds__(1024)
+__global__ void __launch_bounds__(128 * kJoinRows)
     kv_attention_join_kernel(KvArgs a, AttentionArgs at, Parts parts, int P) {
     constexpr int F = D / 32;  // features a lane
-    __shared__ float sums[8][3][D], stats[8][3][2];
+    __shared__ float sums[kJoinRows][3][D], stats[kJoinRows][3][2];
     pdl_wait();
     const int p = blockIdx.x % P, head = blockIdx.x / P;
     const int4 join = parts.joins[p];
@@ -510,7 +513,7 @@ __global__ void __launch_bounds__(1024)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quarter = warp & 3;
     const KvSequence q = kv_sequence(a, join.x);
     const int G = at.q_heads / a.kv_heads, rows = q.count * G;
-    for (int r0 = 0; r0 < 8 * NT; r0 += 8) {
+    for (int r0 = 0; r0 < rows; r0 += kJoinRows) {
         const int r = r0 + (warp >> 2);
         const bool live = r < rows;
         float m = kNothing, l = 0.f, v[F] = {};
@@ -623,7 +626,7 @@ cudaError_t launch_decode(const KvArgs &a, const AttentionArgs &at, void *ws, cu
     if ((e = cudaGetLastError()) != cudaSuccess || P == 1) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(P * a.kv_heads));
-    cfg.blockDim = dim3(1024);
+    cfg.blockDim = dim3(128 * kJoinRows);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
