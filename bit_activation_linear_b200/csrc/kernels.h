@@ -156,7 +156,7 @@ struct AttentionArgs {
 };
 // The kernel for prompts (kv_attention_tc.cu) takes more than kDecodeRows rows (new tokens times
 // query heads of a key head), the streaming kernel (kv_attention.cu) the others.
-constexpr int kDecodeRows = 16;
+constexpr int kDecodeRows = 32;
 size_t kv_attention_tc_workspace(const KvArgs &a, const AttentionArgs &at);
 cudaError_t launch_kv_attention_tc(const KvArgs &a, const AttentionArgs &at, void *ws,
                                    cudaStream_t stream, int *launches);

@@ -124,7 +124,7 @@ __device__ __forceinline__ int work_length(const KvArgs &a, const AttentionArgs 
 
 template <int D, int NT>
 __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1)
-    kv_attention_kernel(KvArgs a, AttentionArgs at, Parts parts, int P) {
+    kv_attention_kernel(KvArgs a, AttentionArgs at, Parts parts, int P, int RT) {
     constexpr int ROWS = 8 * NT;
     constexpr int CB = kChunk * D;           // bytes of a chunk of codes
     constexpr int STAGE = 2 * CB + 16;       // K, V and their steps
@@ -137,7 +137,9 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1)
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int n = lane >> 2, t = lane & 3;
-    const int head = blockIdx.x / P, p = blockIdx.x - head * P;
+    // a group of rows: a key head, and one of RT tiles of ROWS rows (neighbours share the codes in L2)
+    const int p = blockIdx.x / (a.kv_heads * RT), group = blockIdx.x - p * a.kv_heads * RT;
+    const int head = group / RT, row0 = (group - head * RT) * ROWS;
     const int G = at.q_heads / a.kv_heads;
     pdl_launch_dependents();
 
@@ -166,7 +168,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1)
     const long long quota = (total + workers - 1) / workers;
     const long long t0 = p * quota, t1 = min(t0 + quota, total);
     if (t0 >= t1) {  // nothing left for this block
-        if (head == 0 && tid == 0 && P > 1) parts.joins[p] = make_int4(-1, 0, 0, 0);
+        if (group == 0 && tid == 0 && P > 1) parts.joins[p] = make_int4(-1, 0, 0, 0);
         return;
     }
     if (mine > 0 && base <= t0 && t0 < base + mine) {
@@ -182,7 +184,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1)
     __syncthreads();
     int s = found[0], c0 = found[1];
     long long at_chunk = t0;  // line position of chunk c0 of sequence s
-    if (head == 0 && tid == 0 && P > 1) parts.joins[p] = make_int4(-1, 0, 0, 0);
+    if (group == 0 && tid == 0 && P > 1) parts.joins[p] = make_int4(-1, 0, 0, 0);
 
     const uint32_t ring = smem_addr(smem) + warp * kStages * STAGE;
     const int code_shift = a.page_shift + (D == 128 ? 7 : 6), scale_shift = a.page_shift - a.block_shift;
@@ -199,10 +201,11 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1)
         const bool out_of_use = !q.valid || q.count > at.max_new;
         if (out_of_use && tid == 0) record_status(a.status, BITNET_ERR_INVALID);
         const int length = out_of_use || q.count == 0 ? 0 : q.length;
-        const int rows = out_of_use ? 0 : q.count * G;
+        const int rows = out_of_use ? 0 : min(q.count * G - row0, ROWS);  // of this tile
         const int chunks = chunks_of(length);
         const int c1 = (int)min((long long)chunks, c0 + (t1 - at_chunk));
-        const int real = length > 0 ? c1 : c0;  // an empty sequence's one chunk is not there
+        // an empty sequence's one chunk is not there; a tile without rows reads nothing
+        const int real = length > 0 && rows > 0 ? c1 : c0;
 
         // ---- the ring ----
         const int first = c0 + warp;
@@ -256,8 +259,8 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1)
             for (int j = 0; j < KW; ++j) w[j] = make_uint2(0, 0);
             if (r < rows) {
                 const uint8_t *src = static_cast<const uint8_t *>(at.Q) +
-                                     2 * ((int64_t)(q.first + r / G) * at.ldq +
-                                          (int64_t)(head * G + r % G) * D);
+                                     2 * ((int64_t)(q.first + (row0 + r) / G) * at.ldq +
+                                          (int64_t)(head * G + (row0 + r) % G) * D);
 #pragma unroll
                 for (int j = 0; j < KW / 4; ++j) {
                     const uint4 *v = reinterpret_cast<const uint4 *>(src + 32 * (t + 4 * j));
@@ -294,9 +297,9 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const int r = 8 * i + 2 * t + k;
-                seen[i][k] = at.causal && r < rows ? length - q.count + r / G + 1 : length;
+                seen[i][k] = at.causal && r < rows ? length - q.count + (row0 + r) / G + 1 : length;
             }
-        const int all_see = at.causal ? length - q.count + 1 : length;
+        const int all_see = at.causal ? length - q.count + row0 / G + 1 : length;
 
         float o[NT][MT][4], m[NT][2], l[NT][2];
 #pragma unroll
@@ -473,7 +476,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1)
             }
             if (whole) {
                 const float inv = lr == 0.f ? 0.f : __fdividef(1.f, lr);
-                const int64_t token = q.first + r / G, qh = head * G + r % G;
+                const int64_t token = q.first + (row0 + r) / G, qh = head * G + (row0 + r) % G;
                 *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(at.Y) +
                                            2 * (token * at.ldy + qh * D + d)) =
                     make_uint2(bf16x2_of(v.x * inv, v.y * inv), bf16x2_of(v.z * inv, v.w * inv));
@@ -481,13 +484,13 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1)
                     at.lse[token * at.q_heads + qh] =
                         lr == 0.f ? -INFINITY : (mr + log2_approx(lr)) * kLn2;
             } else {
-                const int64_t row = ((int64_t)slot * a.kv_heads + head) * ROWS + r;
+                const int64_t row = ((int64_t)slot * a.kv_heads * RT + group) * ROWS + r;
                 *reinterpret_cast<float4 *>(parts.sums + row * D + d) = v;
                 if (d == 0) *reinterpret_cast<float2 *>(parts.stats + 2 * row) = make_float2(mr, lr);
             }
         }
         // a sequence that begins in this range and ends in a later one is joined behind this block
-        if (head == 0 && tid == 0 && c0 == 0 && c1 < chunks)
+        if (group == 0 && tid == 0 && c0 == 0 && c1 < chunks)
             parts.joins[p] = make_int4(s, (int)((at_chunk + chunks - 1) / quota) - p + 1, slot, 0);
         __syncthreads();  // the sums have been read: the ring may be filled again
         at_chunk += c1 - c0;
@@ -503,16 +506,17 @@ constexpr int kJoinRows = 4;
 
 template <int D, int NT>
 __global__ void __launch_bounds__(128 * kJoinRows)
-    kv_attention_join_kernel(KvArgs a, AttentionArgs at, Parts parts, int P) {
+    kv_attention_join_kernel(KvArgs a, AttentionArgs at, Parts parts, int P, int RT) {
     constexpr int F = D / 32;  // features a lane
     __shared__ float sums[kJoinRows][3][D], stats[kJoinRows][3][2];
     pdl_wait();
-    const int p = blockIdx.x % P, head = blockIdx.x / P;
+    const int p = blockIdx.x % P, group = blockIdx.x / P, head = group / RT;
+    const int row0 = (group - head * RT) * 8 * NT;
     const int4 join = parts.joins[p];
     if (join.x < 0) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quarter = warp & 3;
     const KvSequence q = kv_sequence(a, join.x);
-    const int G = at.q_heads / a.kv_heads, rows = q.count * G;
+    const int G = at.q_heads / a.kv_heads, rows = min(q.count * G - row0, 8 * NT);
     for (int r0 = 0; r0 < rows; r0 += kJoinRows) {
         const int r = r0 + (warp >> 2);
         const bool live = r < rows;
@@ -521,7 +525,7 @@ __global__ void __launch_bounds__(128 * kJoinRows)
 #pragma unroll 4
             for (int i = quarter; i < join.y; i += 4) {
                 const int64_t slot = i == 0 ? join.z : 2 * (p + i);
-                const int64_t row = (slot * a.kv_heads + head) * (8 * NT) + r;
+                const int64_t row = (slot * a.kv_heads * RT + group) * (8 * NT) + r;
                 const float2 ml = *reinterpret_cast<const float2 *>(parts.stats + 2 * row);
                 float u[F];
                 if constexpr (F == 4) {
@@ -560,7 +564,7 @@ __global__ void __launch_bounds__(128 * kJoinRows)
                 m = mn;
             }
             const float inv = l == 0.f ? 0.f : __fdividef(1.f, l);
-            const int64_t token = q.first + r / G, qh = head * G + r % G;
+            const int64_t token = q.first + (row0 + r) / G, qh = head * G + (row0 + r) % G;
             uint8_t *Y = static_cast<uint8_t *>(at.Y) + 2 * (token * at.ldy + qh * D + F * lane);
             uint32_t y[F / 2];
 #pragma unroll
@@ -577,36 +581,41 @@ __global__ void __launch_bounds__(128 * kJoinRows)
     }
 }
 
-// Rows a sequence and key head can have, as tiles of 8 (0: too many for the kernel above).
-int row_tiles(const KvArgs &a, const AttentionArgs &at) {
+// How the rows of a sequence and key head are cut: RT tiles of 8 * nt rows; nt 0 for the other kernel.
+struct RowTiles {
+    int nt, RT;
+};
+RowTiles row_tiles(const KvArgs &a, const AttentionArgs &at) {
     const int64_t rows = (int64_t)at.max_new * (at.q_heads / a.kv_heads);
-    return rows <= 8 ? 1 : rows <= kDecodeRows ? 2 : 0;
+    if (rows > kDecodeRows) return {0, 0};
+    return rows <= 8 ? RowTiles{1, 1} : RowTiles{2, (int)(rows + 15) / 16};
 }
 
-// Blocks per key head: as many as fill the SMs, no more than the longest batch that the page table
-// allows can use.
-int worker_blocks(const KvArgs &a, int nt) {
-    const int64_t fill = kSms * (nt == 1 ? 2 : 1) / a.kv_heads;
+// Blocks per key head and row tile: as many as fill the SMs, no more than the longest batch that the
+// page table allows can use.
+int worker_blocks(const KvArgs &a, RowTiles t) {
+    const int64_t fill = kSms * (t.nt == 1 ? 2 : 1) / (a.kv_heads * t.RT);
     const int64_t most = ((int64_t)a.batch * ((int64_t)a.max_pages << a.page_shift) / kChunk +
                           a.batch + kMinChunks - 1) / kMinChunks;
     const int64_t p = fill < most ? fill : most;
     return p < 1 ? 1 : (int)p;
 }
 
-size_t part_floats(const KvArgs &a, int nt, int P) {
-    return (size_t)2 * P * a.kv_heads * 8 * nt;  // rows of partial sums
+size_t part_rows(const KvArgs &a, RowTiles t, int P) {  // rows of partial sums
+    return (size_t)2 * P * a.kv_heads * t.RT * 8 * t.nt;
 }
 
 template <int D, int NT>
 cudaError_t launch_decode(const KvArgs &a, const AttentionArgs &at, void *ws, cudaStream_t stream,
                           int *launches) {
-    const int P = worker_blocks(a, NT);
+    const RowTiles t = row_tiles(a, at);
+    const int P = worker_blocks(a, t);
     constexpr int ring = kWarps * kStages * (2 * kChunk * D + 16);
     constexpr int join = kWarps * 8 * NT * (D + 4) * 4;
     constexpr int smem = ring > join ? ring : join;
     Parts parts = {};
     if (P > 1) {
-        const size_t rows = part_floats(a, NT, P);
+        const size_t rows = part_rows(a, t, P);
         parts.sums = static_cast<float *>(ws);
         parts.stats = parts.sums + rows * D;
         parts.joins = reinterpret_cast<int4 *>(parts.stats + rows * 2);
@@ -621,11 +630,12 @@ cudaError_t launch_decode(const KvArgs &a, const AttentionArgs &at, void *ws, cu
         if (e != cudaSuccess) return e;
         configured[dev] = true;
     }
-    kern<<<(unsigned)(P * a.kv_heads), 32 * kWarps, smem, stream>>>(a, at, parts, P);
+    const unsigned grid = (unsigned)(P * a.kv_heads * t.RT);
+    kern<<<grid, 32 * kWarps, smem, stream>>>(a, at, parts, P, t.RT);
     *launches = 1;
     if ((e = cudaGetLastError()) != cudaSuccess || P == 1) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(P * a.kv_heads));
+    cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(128 * kJoinRows);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -634,21 +644,21 @@ cudaError_t launch_decode(const KvArgs &a, const AttentionArgs &at, void *ws, cu
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     *launches = 2;
-    return cudaLaunchKernelEx(&cfg, kv_attention_join_kernel<D, NT>, a, at, parts, P);
+    return cudaLaunchKernelEx(&cfg, kv_attention_join_kernel<D, NT>, a, at, parts, P, t.RT);
 }
 
 }  // namespace
 
 size_t kv_attention_workspace(const KvArgs &a, const AttentionArgs &at) {
-    const int nt = row_tiles(a, at);
-    if (nt == 0) return kv_attention_tc_workspace(a, at);
-    const int P = worker_blocks(a, nt);
-    return P == 1 ? 0 : part_floats(a, nt, P) * (a.head_dim + 2) * 4 + (size_t)P * sizeof(int4);
+    const RowTiles t = row_tiles(a, at);
+    if (t.nt == 0) return kv_attention_tc_workspace(a, at);
+    const int P = worker_blocks(a, t);
+    return P == 1 ? 0 : part_rows(a, t, P) * (a.head_dim + 2) * 4 + (size_t)P * sizeof(int4);
 }
 
 cudaError_t launch_kv_attention(const KvArgs &a, const AttentionArgs &at, void *ws,
                                 cudaStream_t stream, int *launches) {
-    switch (row_tiles(a, at)) {
+    switch (row_tiles(a, at).nt) {
         case 1:
             return a.head_dim == 64 ? launch_decode<64, 1>(a, at, ws, stream, launches)
                                     : launch_decode<128, 1>(a, at, ws, stream, launches);

@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- Q: a warp a row (four under way), scaled by a power of two to below 2, as fp16 ----
     constexpr int WQ = D / 64, WARPS = kThreads / 32, ROWS = 4;
 #pragma unroll 1
-    for (int r1 = warp; r1 < kRows; r1 += ROWS * WARPS) {
+    for (int r1 = warp; r1 < rows; r1 += ROWS * WARPS) {
         uint32_t w[ROWS][WQ];
 #pragma unroll
         for (int k = 0; k < ROWS; ++k) {
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < WQ; ++j) mx = __vmaxu2(mx, w[k][j] & 0x7FFF7FFFu);
             mx = __reduce_max_sync(0xFFFFFFFFu, max(mx & 0xFFFFu, mx >> 16));
-            if (r >= kRows) continue;
+            if (r >= rows) continue;  // what lies in rows that are not there goes nowhere
             float up, down;
             row_scaling(mx, down, up);
 #pragma unroll
@@ -397,11 +397,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r = i * kTile + (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + i * kTile + lanes, to = tmem + 2 * kTile + i * D + lanes;
-        const float rowf = sh.rowf[r];
         const bool live = r < rows;
+        const float rowf = live ? sh.rowf[r] : 0.f;
         // rows that are not there see everything and are dropped
         const int seen = !live ? INT32_MAX : at.causal ? q.length - q.count + token_of(r) + 1 : q.length;
-        float m = kNothing, l = 0.f;
+        float m = live ? kNothing : 0.f, l = 0.f;  // (a row that is not there never moves its maximum)
         const int ni = i ? n[1] : n[0], all_see = i ? seen_first[1] : seen_first[0];
         // One step in blocks of 32 tokens, with the maximum so far.  A weight that it makes larger than
         // 2^12 shows in the sum of its group: no scan for the maximum is needed.  Only then (or for
@@ -613,12 +613,15 @@ int64_t tc_units(const KvArgs &a, const AttentionArgs &at) {
     return ((int64_t)a.tokens * (at.q_heads / a.kv_heads) >> 8) + a.batch;
 }
 
-// Pieces that a row's cache is cut into: enough to fill the SMs, none shorter than four steps of
-// the longest sequence that the page table allows.
+// Pieces that a row's cache is cut into, none shorter than four steps of the longest sequence that
+// the page table allows.  Prompts: enough to fill the SMs once (pieces of 256 rows cost 130 KB of
+// partial sums each).  Few rows (one tile at most): enough for two rounds of the SMs, which evens
+// out ragged lengths.
 int tc_splits(const KvArgs &a, const AttentionArgs &at) {
     const int64_t blocks = tc_units(a, at) * a.kv_heads;
     const int64_t steps = ((int64_t)a.max_pages << a.page_shift) / kTile;
-    int64_t n = kSms / (blocks < 1 ? 1 : blocks);
+    const bool few = (int64_t)at.max_new * (at.q_heads / a.kv_heads) <= kTile;
+    int64_t n = few ? (2 * kSms + blocks - 1) / blocks : kSms / blocks;
     if (n > steps / 4) n = steps / 4;
     return n < 1 ? 1 : (int)n;
 }
