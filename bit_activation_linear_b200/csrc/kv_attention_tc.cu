@@ -1,4 +1,4 @@
-// kv_attention_tc.cu -- attention of prompts (more than 16 rows a sequence and key head) over the
+// kv_attention_tc.cu -- attention of prompts (more than 32 rows a sequence and key head) over the
 // paged 8-bit K/V cache, on the tensor cores.  The formulas, the way codes become fp16 and the way
 // d_V goes into the weights are those of kv_attention.cu.
 //
@@ -17,6 +17,12 @@
 // The fp16 weights overwrite the first half of their scores.  The MMAs of one tile execute in the
 // order they are issued: W_i V of step j, then Q_i K^T of step j + 1, so S_i's arrival also says
 // that the O_i before it is complete, and the rare rescaling of O_i needs no barrier of its own.
+//
+// What bounds it: a step of 128 tokens takes about 5000 cycles, the MMAs in it 2048 and the
+// exponentials 2160 (16 a clock and SM): the chain scores -> softmax -> weights -> MMA of a tile is
+// latency-bound with one warp of each tile on a scheduler; the tiles run half a step apart so
+// that one's MMAs lie under the other's softmax.  6001 tokens over 7001 with 16 heads of 128: 279 us,
+// 705 TFLOP/s; 8192 tokens, 32 heads: 796 TFLOP/s; heads of 64: 447 TFLOP/s.
 //
 // Every wait is bounded; after a time-out (recorded) each role leaves its loop and all meet at the
 // end, where tensor memory is freed.

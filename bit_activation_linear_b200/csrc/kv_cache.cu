@@ -14,6 +14,9 @@
 // A NaN or an infinity makes its block's step NaN or infinite (the maximum is taken on the bit
 // patterns, which order NaN above everything) until the block is written anew: attention over it
 // gives NaN instead of a plausible number.
+// Both kernels move 3 bytes a state and are bound by HBM for many tokens (read back of 44 000 tokens
+// of 8 heads: 52 us, 5.2 TB/s), by launch and dependent loads for few (one token for each of 64
+// sequences: 3.9 us; 8700 tokens: 15 us).
 #include "kv_common.cuh"
 
 namespace bitnet {
@@ -83,7 +86,7 @@ __device__ __forceinline__ uint32_t recode4(uint32_t c, float r) {
 }
 
 // SMALL: scale blocks of 16 tokens, whose states stay in registers between the maximum and the
-// codes; longer blocks are read twice (the second time from the cache).
+// codes; longer blocks do not fit there and are read twice (the second time from L1 or L2).
 template <int D, bool SMALL>
 __global__ void __launch_bounds__(32 * kWarps, 4)
     kv_append_kernel(KvArgs a, const uint8_t *__restrict__ K, int64_t ldk,
@@ -226,8 +229,8 @@ __global__ void __launch_bounds__(32 * kWarps, 6)
 }  // namespace
 
 // The grid over spans and (K or V, head) pairs, a warp a pair: long spans where there are enough of
-// them to fill the GPU (kFill blocks), else spans of one `shortest`, and the pairs dealt to several
-// blocks.
+// them to fill the GPU (kFill blocks; read back of 44 000 tokens 52 us, 63 us with 16), else spans of
+// one `shortest`, and the pairs dealt to several blocks (append of 8700 tokens 15 us, 25 us with 64).
 constexpr int kFill = 4 * kSms;
 
 static dim3 span_grid(const KvArgs &a, int shortest, int &shift) {

@@ -8,6 +8,12 @@
 //   codes of y: absmax INT8 or absmean INT4, as act_quant_plain_kernel.
 // The norm reads the ROUNDED h: it is what the stream holds and what every later reader sees, so
 // one call gives what the addition followed by bitnet_act_quant_norm gives.
+//
+// Bound by HBM: 6 bytes and the code an element, read once.  A row stays in the registers of its
+// threads between the addition and the codes (4 chunks of 8 values each, so K / 32 threads a row).
+// Measured on B200: 16383 x 4096 in 72 .. 75 us (6.2 .. 6.5 TB/s), 4096 x 2048 in 12 .. 14 us, one row
+// in the 3.4 us of a launch.  Rows above K = 32768 need more threads than a block has and are read
+// back: 4.2 TB/s at 33024 against 4.4 TB/s at 32768.
 #include "common.cuh"
 #include "kernels.h"
 

@@ -506,12 +506,14 @@ int bitnet_kv_cache_read(const bitnet_kv_cache *cache, const bitnet_kv_batch *ba
  *   y = sum_t exp(s_t) c_V(t) d_V(t) / sum_t exp(s_t)  (bf16),   lse = log sum_t exp(s_t)  (fp32)
  * A row that sees no token (a length of 0, or fewer tokens than new ones) gives y = 0, lse = -inf.
  * The scores are exact products of Q (bf16, scaled by a power of two a row) and the codes, summed
- * in fp32; the weights are rounded to 11 bits for the product with the V codes, relative to the
+ * in fp32; the weights are rounded to 11 bits for the product with the V codes, or to 2^-25 of the
  * row's largest weight; sums are fp32.  Results do not depend on timing.
- * Q_dev, Y_dev  bf16 rows of q_heads * head_dim, ldq / ldy elements apart (multiples of 8).
+ * Q_dev, Y_dev  bf16 rows of q_heads * head_dim, ldq / ldy elements apart (multiples of 8); they
+ *               must not overlap.
  * q_heads       kv_heads times 1 .. 128.
- * max_new       no sequence has more new tokens than this (>= 1): it chooses the kernel.  A
- *               sequence that has more is invalid.
+ * max_new       no sequence has more new tokens than this (>= 1): it chooses the kernel (up to 32
+ *               rows, new tokens times query heads of a key head, stream the cache; more run on
+ *               the tensor cores in tiles of 128 rows).  A sequence that has more is invalid.
  * scale         finite and > 0, usually 1 / sqrt(head_dim).
  * lse_dev       out: float [tokens][q_heads], or NULL.
  * ws_dev        scratch of ws_bytes >= bitnet_kv_attention_workspace_bytes(...) (0 for arguments

@@ -336,7 +336,7 @@ def check_attention(B, b, cache, got, q_heads, causal=True, scale=None, max_new=
 
 
 @pytest.mark.parametrize("dim", [64, 128])
-@pytest.mark.parametrize("group", [1, 3, 4, 8, 12, 16])
+@pytest.mark.parametrize("group", [1, 3, 4, 8, 12, 16, 17, 32, 33])
 def test_attention_single_tokens_ragged(B, dim, group):
     rng = np.random.default_rng(dim + group)
     lengths = [1, 15, 16, 17, 300, 64, 129]
@@ -478,6 +478,27 @@ def test_attention_strided_rows_and_hints(B):
         assert np.all(o[:, :8] == 7) and np.all(o[:, 8 + q_heads * dim:] == 7)
         o = o[:, 8:8 + q_heads * dim].reshape(y.shape)
         assert np.all(np.abs(o - y) <= BF16_HALF * np.abs(y) + tol_y * (1 + BF16_HALF))
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_sequences_that_share_pages(B, new):
+    """A common prefix in pages that two sequences read gives what copies of the pages give."""
+    rng = np.random.default_rng(new)
+    heads, dim, page = 2, 64, 32
+    cache = B.KvCache.empty(12, heads, dim, page, 16)
+    table = ints([[3, 7, 1, 2], [5, 6, 0, 4]])
+    prefix = bf16(rng.standard_normal((64, heads * dim)))[0]
+    tails = bf16(rng.standard_normal((2 * new, heads * dim)))[0]
+    twice = torch.cat([prefix, prefix])
+    B.bitnet_kv_cache_append(cache, twice, twice, ints([0, 64, 128]), ints([64, 64]), table)
+    meta = ints([0, new, 2 * new]), ints([64 + new, 64 + new])
+    B.bitnet_kv_cache_append(cache, tails, tails, *meta, table)
+    Q = bf16(rng.standard_normal((2 * new, 4 * dim)))[0]
+    want = B.bitnet_kv_attention(cache, Q, 4, *meta, table, new, want_lse=True)
+    shared = ints([[3, 7, 1, 2], [3, 7, 0, 4]])
+    got = B.bitnet_kv_attention(cache, Q, 4, *meta, shared, new, want_lse=True)
+    B.bitnet_sync_status()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
 def test_offsets_beyond_32_bits(B):
