@@ -402,9 +402,9 @@ __host__ __device__ constexpr uint32_t idesc_i8_s8u8(int M, int N) {
 }
 
 // ------------------------------------------------------------------------------------------
-// Packed fp32x2 arithmetic with an explicit rounding mode: PTX add/mul carrying .rn are never
-// contracted into a fused multiply-add, so a product followed by a sum rounds twice, exactly as
-// two IEEE fp32 operations (the float2 intrinsics alone do not guarantee that).
+// Packed fp32x2 arithmetic with an explicit rounding mode.  A packed product that feeds a packed sum
+// may still become one fused operation, which rounds once (seen on B200 as codes that are off by one
+// at ties): where both roundings matter, take the product with the scalar __fmul_rn.
 // ------------------------------------------------------------------------------------------
 __device__ __forceinline__ float2 mul2_rn(float2 a, float2 b) {
     float2 d;

@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1)
             pos += kWarps * kChunk;
         }
 
-        // ---- join the four warps ----
+        // ---- join the warps ----
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll

@@ -539,8 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 32; ++e) v[e] = 0;
                 }
-                if (!live) continue;
-                if (splits == 1) {
+                if (live && splits == 1) {
                     uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(at.Y) +
                                                            2 * (token * at.ldy + qh * D + 32 * b));
 #pragma unroll
@@ -552,12 +551,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                                              __uint_as_float(v[8 * e + 2 * k + 1]) * inv);
                         dst[e] = make_uint4(y[0], y[1], y[2], y[3]);
                     }
-                } else {
+                } else if (live) {
                     uint4 *dst = reinterpret_cast<uint4 *>(parts.sums + piece * D + 32 * b);
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
                         dst[e] = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
                 }
+                __syncwarp();  // the next load takes the whole warp
             }
             if (live) {
                 if (splits > 1)
