@@ -15,8 +15,8 @@
 // patterns, which order NaN above everything) until the block is written anew: attention over it
 // gives NaN instead of a plausible number.
 // Both kernels move 3 bytes a state and are bound by HBM for many tokens (read back of 44 000 tokens
-// of 8 heads: 52 us, 5.2 TB/s), by launch and dependent loads for few (one token for each of 64
-// sequences: 3.9 us; 8700 tokens: 15 us).
+// of 8 heads: 49 us, 5.6 TB/s), by launch and dependent loads for few (one token for each of 64
+// sequences: 3.7 us; 8700 tokens: 14 us).
 #include "kv_common.cuh"
 
 namespace bitnet {
@@ -181,8 +181,16 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
 
 // Reads back a sequence's last tokens, 16 positions of one head at a time.  A scale block is at
 // least 16 tokens, so the 16 share a step.
-__device__ __forceinline__ uint32_t value2(uint32_t two, float d) {  // two codes -> two bf16
-    return bf16x2_of(__fmul_rn((float)(int8_t)two, d), __fmul_rn((float)(int8_t)(two >> 8), d));
+// Four codes as two pairs of bf16 values.  The byte c xor 0x80 under 0x4B0000 is the float 2^23 + 128
+// + c: one byte permutation and an exact subtraction (int to float conversions, 16 a clock and SM,
+// kept half of the reading time busy).
+__device__ __forceinline__ uint2 values4(uint32_t codes, float d) {
+    const uint32_t u = codes ^ 0x80808080u;
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        v[i] = __fmul_rn(__uint_as_float(prmt(u, 0x4B000000u, 0x7540u + i)) - 8388736.f, d);
+    return make_uint2(bf16x2_of(v[0], v[1]), bf16x2_of(v[2], v[3]));
 }
 
 template <int D>
@@ -217,10 +225,10 @@ __global__ void __launch_bounds__(32 * kWarps, 6)
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const int t = sub + i * TPW;
-                if (start + t >= x.lo && start + t < x.hi)
-                    reinterpret_cast<uint4 *>(out + t * ld)[off] =
-                        make_uint4(value2(c[i].x, d), value2(c[i].x >> 16, d), value2(c[i].y, d),
-                                   value2(c[i].y >> 16, d));
+                if (start + t >= x.lo && start + t < x.hi) {
+                    const uint2 lo = values4(c[i].x, d), hi = values4(c[i].y, d);
+                    reinterpret_cast<uint4 *>(out + t * ld)[off] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+                }
             }
         }
     }
@@ -230,7 +238,8 @@ __global__ void __launch_bounds__(32 * kWarps, 6)
 
 // The grid over spans and (K or V, head) pairs, a warp a pair: long spans where there are enough of
 // them to fill the GPU (kFill blocks; read back of 44 000 tokens 52 us, 63 us with 16), else spans of
-// one `shortest`, and the pairs dealt to several blocks (append of 8700 tokens 15 us, 25 us with 64).
+// one `shortest` (append of 8700 tokens 15 us, 25 us with 64); then the pairs are dealt to several
+// blocks, up to three times kFill in all (those two 49 and 14 us).
 constexpr int kFill = 4 * kSms;
 
 static dim3 span_grid(const KvArgs &a, int shortest, int &shift) {
@@ -238,7 +247,7 @@ static dim3 span_grid(const KvArgs &a, int shortest, int &shift) {
     shift = shortest < kSpanShift && spans(kSpanShift) < kFill ? shortest
                                                                 : max(shortest, kSpanShift);
     const int64_t x = spans(shift), most = (2 * a.kv_heads + kWarps - 1) / kWarps;
-    const int64_t y = (kFill + x - 1) / x;
+    const int64_t y = (3 * kFill + x - 1) / x;
     return dim3((unsigned)x, (unsigned)(y < most ? y : most));
 }
 
