@@ -687,6 +687,39 @@ def test_attention_on_two_streams_and_in_replayed_graphs(B, new):
     B.bitnet_sync_status()
 
 
+@pytest.mark.parametrize("own_stream", [False, True])
+def test_chains_of_calls_that_nothing_waits_between(B, own_stream):
+    """Writes and attention of growing sequences, one call after the other, give what they give with
+    a synchronisation behind every call (the kernels are launched before the ones they follow end)."""
+    heads, dim, group = 2, 128, 4
+    stream = torch.cuda.Stream() if own_stream else torch.cuda.current_stream()
+    results = []
+    with torch.cuda.stream(stream):
+        table = torch.arange(80, dtype=torch.int32, device="cuda").view(4, 20)
+        for wait in (False, True):
+            cache = B.KvCache.empty(80, heads, dim)
+            gen = torch.Generator(device="cuda").manual_seed(1)
+            rng = np.random.default_rng(2)
+            length, out = np.zeros(4, int), []
+            for step in range(40):
+                new = rng.integers(0, 4 if step % 10 else 60, 4)
+                length = length + new
+                if not new.sum():
+                    continue
+                meta = ints(np.concatenate([[0], np.cumsum(new)])), ints(length), table
+                qkv = torch.randn((int(new.sum()), (group + 2) * heads * dim), generator=gen,
+                                  device="cuda").bfloat16()
+                q, k, v = qkv.split([group * heads * dim, heads * dim, heads * dim], 1)
+                B.bitnet_kv_cache_append(cache, k, v, *meta)
+                out += B.bitnet_kv_attention(cache, q, group * heads, *meta, int(new.max()),
+                                             want_lse=True)
+                if wait:
+                    torch.cuda.synchronize()
+            B.bitnet_sync_status()
+            results.append(out)
+    assert all(torch.equal(x, y) for x, y in zip(*results))
+
+
 def test_a_layer_step_residual_norm_qkv_cache_attention(B):
     """The operators one after the other as a decoder layer runs them: residual norm and Q/K/V
     product, cache write, attention, H-BitLinear output projection; a prompt, then single tokens,
