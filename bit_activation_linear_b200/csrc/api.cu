@@ -883,6 +883,7 @@ size_t bitnet_kv_attention_workspace_bytes(const bitnet_kv_cache *cache,
     KvArgs a;
     AttentionArgs at;
     if (kv_args(cache, batch, &a) || attention_args(a, q_heads, max_new, &at)) return 0;
+    if (a.tokens == 0 || a.batch == 0) return 0;  // nothing to launch, and no blocks to size it by
     return round256(kv_attention_workspace(a, at));
 }
 

@@ -1,6 +1,7 @@
 """Refusals and sizes of the residual norm, K/V cache and attention entries (no GPU needed): every
 call here is answered by the host checks."""
 import ctypes
+import os
 
 import pytest
 import torch
@@ -101,6 +102,21 @@ def test_empty_calls_are_answered_without_a_device(B, lib):
     for change in (dict(tokens=0), dict(batch=0, q_start=None, kv_len=None, page_table=None)):
         for call in (append, read, attend):
             assert call(lib, cache(B), batch(B, **change)) == 0
+
+
+@pytest.mark.parametrize("max_new", [1, 8, 9, 500])
+@pytest.mark.parametrize("change", [dict(tokens=0), dict(tokens=0, batch=0), dict(batch=0),
+                                    dict(batch=0, tokens=2)])
+def test_empty_batches_need_no_workspace(B, lib, change, max_new):
+    """Few and many rows (both attention kernels), asked in a child: a signal there is a failure
+    here and does not end the run."""
+    pid = os.fork()
+    if pid == 0:
+        need = lib.bitnet_kv_attention_workspace_bytes(cache(B), batch(B, **change), 16, max_new)
+        os._exit(need != 0)
+    assert os.waitpid(pid, 0)[1] == 0
+    assert attend(lib, cache(B), batch(B, **change), heads=16, max_new=max_new, ldq=2048, ldy=2048,
+                  ws=None, ws_bytes=0) == 0
 
 
 def test_attention_workspace_size_and_refusal(B, lib):

@@ -648,6 +648,24 @@ def test_empty_calls_do_nothing(B):
     same_cache(got, cache)
 
 
+@pytest.mark.parametrize("max_new", [1, 9, 300])
+def test_empty_batches_of_either_kernel_do_nothing(B, max_new):
+    """A scheduler with nobody to serve: the call allocates its own workspace."""
+    rng = np.random.default_rng(1)
+    b, cache, got = filled(B, rng, [5], [1], 4, 64, 16, 16)
+    nobody = (ints([0]), ints([]), torch.empty((0, 3), dtype=torch.int32, device="cuda"))
+    for tokens in (0, 2):
+        Q = torch.full((tokens, 16 * 64), 7.0, dtype=torch.bfloat16, device="cuda")
+        Y = Q.clone()
+        assert B.bitnet_kv_attention_workspace_bytes(got, tokens, 0, 3, 16, max_new) == 0
+        B.bitnet_kv_attention(got, Q, 16, *nobody, max_new, Y=Y)
+        assert torch.equal(Y, Q)
+    none = torch.empty((0, 16 * 64), dtype=torch.bfloat16, device="cuda")
+    B.bitnet_kv_attention(got, none, 16, ints([0, 0]), ints([5]), ints(b.table), max_new)
+    B.bitnet_sync_status()
+    same_cache(got, cache)
+
+
 @pytest.mark.parametrize("new", [1, 24])
 def test_attention_on_two_streams_and_in_replayed_graphs(B, new):
     """Two calls at once with a workspace each; a graph replayed with other lengths, pages and
