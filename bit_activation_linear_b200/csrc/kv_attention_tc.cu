@@ -450,6 +450,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const bool over = fmaxf(sg[0], sg[1]) > 4096.f || m == kNothing;
                     if (moved || !__any_sync(0xFFFFFFFFu, over)) break;
                     moved = true;
+                    // earlier weights of this step, and O_i where it was scaled before, are read back
+                    // below: stores to tensor memory are only ordered before loads by this wait
+                    tmem_wait_st();
                     float top = kNothing;
 #pragma unroll
                     for (int e = 0; e < 32; ++e)

@@ -575,6 +575,45 @@ def test_attention_scores_that_keep_growing_and_falling(B):
             assert np.all(np.abs(lse.cpu().numpy() - l) <= tol_l)
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("jump", [9, 13])
+@pytest.mark.parametrize("run", [16, 32, 48])
+def test_attention_maxima_that_move_several_times_in_a_step(B, dim, jump, run):
+    """Scores that rise by 2^jump every `run` tokens: the prompt kernel scales the weights it has
+    already stored for a step of 128 tokens, and the sums of earlier steps, up to eight times in that
+    step.  The highest tokens have zero V codes in half of the features, whose outputs are then made
+    of what was scaled."""
+    heads, page, block = 2, 64, 16
+    lengths, new = [130, 200, 333, 460], [40, 33, 60, 35]
+    rng = np.random.default_rng(jump + run)
+    b = Batch(lengths, new, page, rng)
+    cache = ref.Cache(b.pages, heads, dim, page, block, rng)
+    for s, length in enumerate(lengths):
+        for t in range(length):
+            at = (b.table[s, t // page], slice(None), t % page)
+            cache.codes[0][at] = 0
+            level = t // run
+            cache.codes[0][at + (0,)] = 4 * level        # times a step of jump / 4, in powers of two
+            cache.codes[1][at] = rng.integers(60, 120, (heads, dim))
+            if level == (length - 1) // run:
+                cache.codes[1][at][:, : dim // 2] = 0
+    cache.steps[0][:] = jump / 4
+    cache.steps[1][:] = 0.01
+    got = to_device(B, cache)
+    q = np.zeros((b.tokens, heads, dim), np.float32)
+    q[:, :, 0] = 1
+    Q, q = bf16(q)
+    scale = float(np.float32(np.log(2.0)))
+    Y, lse = B.bitnet_kv_attention(got, Q.flatten(1), heads, *b.device(), max(new), scale=scale,
+                                   want_lse=True)
+    B.bitnet_sync_status()
+    y, l, tol_y, tol_l = ref.attention(cache, q.astype(np.float64), b.q_start, b.kv_len, b.table,
+                                       scale, True)
+    got_y = Y.float().cpu().numpy().reshape(y.shape)
+    assert np.all(np.abs(got_y - y) <= BF16_HALF * np.abs(y) + tol_y * (1 + BF16_HALF))
+    assert np.all(np.abs(lse.cpu().numpy() - l) <= tol_l)
+
+
 # ----------------------------------------------------------------------------------------
 # what the device finds wrong; streams and graphs
 # ----------------------------------------------------------------------------------------
