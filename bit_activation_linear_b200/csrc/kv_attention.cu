@@ -24,11 +24,15 @@
 // consecutive codes of a token with one 16-byte read.
 //
 // Weights.  d_V varies from block to block, so it belongs to the weight: w_t = exp2(s_t log2 e +
-// log2 d_V(t) - m), m the row's maximum of that sum.  w <= 1 is rounded to fp16 (11 bits, or
-// 2^-25 of the row's largest) for the product with the codes; the denominator sums w_t / d_V(t) in
-// fp32, unrounded.  A block is at least 16 tokens, so a chunk of 16 has one d_K and one d_V.
-// m is only moved when a chunk exceeds it by more than 2^8 (the weights then reach 256, far from
-// fp16's limit): nearly all chunks need one vote instead of a reduction and a rescaling.
+// log2 d_V(t) - m), m a reference that follows the row's maximum of that sum.  w is rounded to fp16
+// for the product with the codes; the denominator sums w_t / d_V(t) in fp32, unrounded.  A block is
+// at least 16 tokens, so a chunk of 16 has one d_K and one d_V.
+// fp16 has 16 binary orders above 1 and 25 below, where a weight that is too small vanishes from the
+// numerator: m is put 7 below the maximum, so the row's largest weight is in (2^6, 2^7] and one of
+// 2^-31 of it is still seen (a token that takes nearly all of the weight, in front of a long cache:
+// with the maximum at 1 the output was several per cent off).  m is only moved when a chunk exceeds 2^15:
+// nearly all chunks need one vote instead of a reduction and a rescaling.  It moves by whole numbers,
+// so rescaling is exact.
 //
 // Work split.  Per key head the chunks of all sequences form one line, cut into equal ranges, one
 // for each of P blocks (P * heads fills the SMs once): ragged batches, single long sequences and
@@ -53,6 +57,8 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kStages = 3;
 constexpr uint32_t kNoPage = 0xFFFFFFFFu;  // a step (a NaN that no product gives)
+constexpr float kTop = 7.f;     // log2 of where a moved reference puts the largest weight, and of
+constexpr float kLimit = 15.f;  // the weight above which it moves
 constexpr int kMinChunks = 32;  // shorter ranges do not repay the second launch (about 4 us)
 
 // The device's view of the partial sums: [2 * P][heads][rows][D] sums, then [..][rows][2] maxima
@@ -375,8 +381,8 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1)
                         for (int k4 = 0; k4 < 4; ++k4)
                             if (pos + n + 8 * (k4 >> 1) >= seen[i][k4 & 1]) sc[i][k4] = -INFINITY;
                     }
-                    over |= fmaxf(sc[i][0], sc[i][2]) > m[i][0] + kSlack ||
-                            fmaxf(sc[i][1], sc[i][3]) > m[i][1] + kSlack;
+                    over |= fmaxf(sc[i][0], sc[i][2]) > m[i][0] + kLimit ||
+                            fmaxf(sc[i][1], sc[i][3]) > m[i][1] + kLimit;
                 }
                 if (__any_sync(0xFFFFFFFFu, over)) {
 #pragma unroll
@@ -387,7 +393,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1)
                             x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
                             x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
                             x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
-                            x = fmaxf(x, m[i][k2]);
+                            x = fmaxf(ceilf(x) - kTop, m[i][k2]);
                             const float keep = exp2_approx(m[i][k2] - x);
                             m[i][k2] = x;
                             l[i][k2] *= keep;

@@ -42,6 +42,11 @@ constexpr int kThreads = 20 * 32;         // warps 18 and 19 only complete the l
 // Registers: launched with 96 a thread (20 warps); 8 softmax warps take 144, the other 12 keep 64:
 // 8 * 144 + 12 * 64 = 20 * 96.
 constexpr int kManyRegisters = 144, kFewRegisters = 64;
+// Weights in fp16 as in kv_attention.cu.  Here the sum of a 16-token group shows that one of them is
+// too large for fp16 (65504): the reference moves where it exceeds 60 * 2^10, and then puts the
+// largest weight in (2^7, 2^8].  Higher would see smaller weights but moves more often: 6001 tokens
+// over 7001 take 278.6 us at 2^6, 279.5 at 2^8, 287 at 2^9 (with 2^15).
+constexpr float kTop = 8.f, kMostSum = 61440.f;
 
 __device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                            uint32_t accumulate) {
@@ -407,11 +412,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float rowf = live ? sh.rowf[r] : 0.f;
         // rows that are not there see everything and are dropped
         const int seen = !live ? INT32_MAX : at.causal ? q.length - q.count + token_of(r) + 1 : q.length;
-        float m = live ? kNothing : 0.f, l = 0.f;  // (a row that is not there never moves its maximum)
+        float m = live ? kNothing : 0.f, l = 0.f;  // (a row that is not there has a reference)
         const int ni = i ? n[1] : n[0], all_see = i ? seen_first[1] : seen_first[0];
-        // One step in blocks of 32 tokens, with the maximum so far.  A weight that it makes larger than
-        // 2^12 shows in the sum of its group: no scan for the maximum is needed.  Only then (or for
-        // a row's first block) the maximum moves, the block is made again, and what the old one went
+        // One step in blocks of 32 tokens, with the reference so far.  A weight that it makes larger
+        // than kMostSum shows in the sum of its group: no scan for the maximum is needed.  Only then (or for
+        // a row's first block) the reference moves, the block is made again, and what the old one went
         // into is scaled: the sum, O_i, the step's earlier weights.  `sees` of the 128 tokens are seen.
         // The code is kept short (loops, one copy of the block): unrolled it was 110 KB, and fetching
         // instructions bound the kernel.
@@ -447,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         sum[0] = __fadd2_rn(sum[0], sum[1]);
                         sg[h] = sum[0].x + sum[0].y;
                     }
-                    const bool over = fmaxf(sg[0], sg[1]) > 4096.f || m == kNothing;
+                    const bool over = fmaxf(sg[0], sg[1]) > kMostSum || m == kNothing;
                     if (moved || !__any_sync(0xFFFFFFFFu, over)) break;
                     moved = true;
                     // earlier weights of this step, and O_i where it was scaled before, are read back
@@ -458,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int e = 0; e < 32; ++e)
                         if (!PART || e < left)
                             top = fmaxf(top, fmaf(__uint_as_float(v[e]), f[e / 16], e < 16 ? g0.y : g1.y));
-                    const float mn = over ? fmaxf(m, top) : m;
+                    const float mn = over ? fmaxf(m, ceilf(top) - kTop) : m;
                     const float keep = exp2_approx(m - mn);
                     m = mn;
                     l *= keep;

@@ -76,9 +76,8 @@ __device__ __forceinline__ int64_t kv_scale_at(const KvArgs &a, int page, int he
 constexpr int kChunk = 16;      // tokens: a scale block is a whole number of chunks
 constexpr int kSms = 148;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kNothing = -3.0e38f;  // the maximum of a row that has seen nothing
+constexpr float kNothing = -3.0e38f;  // the reference of a row that has seen nothing
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kSlack = 8.f;   // log2 of how far a weight may exceed 1 before the maximum moves
 
 __device__ __forceinline__ uint32_t sub_1152(uint32_t two) {
     uint32_t d;
@@ -113,8 +112,10 @@ __device__ __forceinline__ void row_scaling(uint32_t mx, float &down, float &up)
     down = 1.f / up;
 }
 
-// d_V as the weights carry it: never 0 (a log2 is taken of it), NaN and infinity as they are.
-__device__ __forceinline__ float v_step(float d) { return d < 1e-30f ? 1e-30f : d; }
+// d_V as the weights carry it: never 0 (a log2 is taken of it), NaN and infinity as they are.  The
+// denominator sums weights of up to 2^15 over d_V: with 2^-90 it stays below 2^126, from where the
+// fast division gives 0, for 2^21 tokens.
+__device__ __forceinline__ float v_step(float d) { return d < 8e-28f ? 8e-28f : d; }
 
 __device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
     uint32_t d;
