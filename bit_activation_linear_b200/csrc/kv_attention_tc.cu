@@ -467,14 +467,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float keep = exp2_approx(m - mn);
                     m = mn;
                     l *= keep;
-                    const uint32_t keep2 = half2_of(keep, keep);
 #pragma unroll 1
                     for (int c16 = 0; c16 < b; ++c16) {
                         tmem_ld_32x32b_x16(ts + 16 * c16, w);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            asm("mul.f16x2 %0, %0, %1;" : "+r"(w[e]) : "r"(keep2));
+                        for (int e = 0; e < 16; ++e) {  // in fp32: fp16 has no factor below 2^-24
+                            const float2 z = float2_of(w[e]);
+                            w[e] = half2_of(z.x * keep, z.y * keep);
+                        }
                         tmem_st_32x32b_x16(ts + 16 * c16, w);
                     }
 #pragma unroll 1

@@ -1,4 +1,5 @@
-"""What the attention kernels' fp16 weights may lose: tokens that hold nearly all of a row's weight.
+"""What the attention kernels' fp16 weights may lose: scores that jump, tokens that hold nearly all of
+a row's weight.
 
 One sequence (or many that share its pages) whose codes and steps are made by hand: the key's first
 feature is the score in powers of two, and V codes that are small where the weight is large show what
@@ -81,6 +82,32 @@ def check(got_y, got_lse, want):
     err = np.abs(got - y)
     assert np.all(err <= 2.0**-8 * np.abs(y) + ty * (1 + 2.0**-8)), (err / np.abs(y)).max()
     assert np.all(np.abs(got_lse.double().cpu().numpy().reshape(lse.shape) - lse) <= tl)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("jump", [8, 10, 14, 17, 20.5, 22, 24, 26])
+def test_a_score_that_jumps_inside_a_step(B, dim, jump):
+    """Flat scores, then one token in a later block of the last step that is 2^jump above them: the
+    prompt kernel has stored the step's earlier weights by then, and scales them."""
+    length, new = 360, 33
+    rng = np.random.default_rng(dim)
+    tokens = -(-length // PAGE) * PAGE
+    k, v = (np.zeros((tokens, dim), np.int8) for _ in range(2))
+    v[:] = rng.integers(20, 120, v.shape)
+    v[321] = 0                                   # position 65 of the step that begins at 256
+    v[321, ::4] = 1
+    k[321, 0] = 100
+    dk = np.full(tokens // BLOCK, jump / 100, np.float32)
+    dv = np.full(tokens // BLOCK, 0.02, np.float32)
+    q = np.zeros((new, 1, dim))
+    q[..., 0] = 1
+    cache = make_cache(B, k, v, dk, dv)
+    Q = torch.from_numpy(q).bfloat16().cuda().flatten(1)
+    table = ints(np.arange(tokens // PAGE))[None]
+    Y, lse = B.bitnet_kv_attention(cache, Q, 1, ints([0, new]), ints([length]), table, new,
+                                   scale=LN2, want_lse=True)
+    B.bitnet_sync_status()
+    check(Y, lse, expected(q, k, v, dk, dv, LN2, length, new))
 
 
 @pytest.mark.parametrize("depth", [18.0, 22.0, 25.5, 27.0])
