@@ -19,7 +19,7 @@
 //
 // Codes to fp16.  A code c of -128 .. 127 xor 0x80 is the byte c + 128; under the byte 0x64 that is
 // the fp16 number 1152 + c, and one subtraction gives c exactly.  q is scaled by a power of two a
-// row to below 2, so bf16 -> fp16 loses nothing but bits below 2^-24; products are then exact and
+// row (row_scaling), so bf16 -> fp16 loses only bits below 2^-38 of the row's largest; products are exact and
 // summed in fp32.  The order of the features inside an mma's k is free, so a lane takes 16
 // consecutive codes of a token with one 16-byte read.
 //
@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1)
         };
 #pragma unroll
         for (int k = 0; k < kStages - 1; ++k) bring();
-        // ---- Q: this lane's features of row n (and n + 8), scaled to below 2 ----
+        // ---- Q: this lane's features of row n (and n + 8), scaled as fp16 ----
         uint32_t qf[NT][2 * KW];
         float rowf[NT][2];  // scale * log2 e / that scaling, rows 2t and 2t + 1
 #pragma unroll

@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc(&sh.tmem, 512);
         tmem_relinquish();
     }
-    // ---- Q: a warp a row (four under way), scaled by a power of two to below 2, as fp16 ----
+    // ---- Q: a warp a row (four under way), scaled by a power of two, as fp16 ----
     constexpr int WQ = D / 64, WARPS = kThreads / 32, ROWS = 4;
 #pragma unroll 1
     for (int r1 = warp; r1 < rows; r1 += ROWS * WARPS) {

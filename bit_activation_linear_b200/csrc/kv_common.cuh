@@ -111,10 +111,14 @@ __device__ __forceinline__ float log2_approx(float x) {
 }
 
 // bf16 pairs of a row of Q (largest magnitude `mx` as bf16 bits): the powers of two that scale it to
-// below 2 and back; 1 for zeros, infinities and NaN (such a row's outputs are NaN).
+// below 2^15, under fp16's limit, and back.  The row's features then keep their bits down to 2^-38 of
+// its largest (scaled to below 2 they kept 2^-24: where a large feature meets zeros in the keys, the
+// scores are made of the small ones).  Rows below 2^-62 are scaled to below 2, so that `up` and the
+// products with it stay normal numbers; 1 for zeros, infinities and NaN (the outputs of a row that
+// has one are NaN).
 __device__ __forceinline__ void row_scaling(uint32_t mx, float &down, float &up) {
-    const uint32_t ex = mx >> 7;
-    up = mx != 0 && ex < 255 ? __uint_as_float(max(ex, 1u) << 23) : 1.f;
+    const uint32_t ex = mx >> 7, at = ex > 64 ? ex - 14 : max(ex, 1u);
+    up = mx != 0 && ex < 255 ? __uint_as_float(at << 23) : 1.f;
     down = 1.f / up;
 }
 

@@ -505,7 +505,8 @@ int bitnet_kv_cache_read(const bitnet_kv_cache *cache, const bitnet_kv_batch *ba
  *   s_t = scale * (q . c_K(t)) * d_K(t),   t <= kv_len - n + i (causal != 0) or t < kv_len
  *   y = sum_t exp(s_t) c_V(t) d_V(t) / sum_t exp(s_t)  (bf16),   lse = log sum_t exp(s_t)  (fp32)
  * A row that sees no token (a length of 0, or fewer tokens than new ones) gives y = 0, lse = -inf.
- * The scores are exact products of Q (bf16, scaled by a power of two a row) and the codes, summed
+ * The scores are exact products of Q (bf16, scaled by a power of two a row and held in fp16: bits
+ * below 2^-38 of the row's largest magnitude are rounded away) and the codes, summed
  * in fp32; the weights (times the steps of V) are rounded to 11 bits for the product with the V
  * codes, or to 2^-31 of the row's largest one; sums are fp32.  Results do not depend on timing.
  * Q_dev, Y_dev  bf16 rows of q_heads * head_dim, ldq / ldy elements apart (multiples of 8); they

@@ -1,5 +1,5 @@
-"""What the attention kernels' fp16 weights may lose: scores that jump, tokens that hold nearly all of
-a row's weight.
+"""What the attention kernels' fp16 weights and queries may lose: scores that jump, tokens that hold
+nearly all of a row's weight, query features of very different size.
 
 One sequence (or many that share its pages) whose codes and steps are made by hand: the key's first
 feature is the score in powers of two, and V codes that are small where the weight is large show what
@@ -135,3 +135,29 @@ def test_small_weights_behind_a_large_one(B, depth, new, batch):
     Y, lse = Y.view(batch, new, dim), lse.view(batch, new)
     for s in {0, batch // 2, batch - 1}:
         check(Y[s], lse[s], want)
+
+
+@pytest.mark.parametrize("small", [2.0**-16, 2.0**-20, 2.0**-24, 2.0**-28])
+@pytest.mark.parametrize("row", [1.0, 2.0**-50, 2.0**60])
+@pytest.mark.parametrize("new", [1, 40])
+def test_query_features_of_very_different_size(B, small, row, new):
+    """One feature of q is far larger than the others, where the keys have zeros: the scores are made
+    of the others.  (Both kernels keep bits down to 2^-38 of the row's largest.)"""
+    length, dim = 200, 64
+    rng = np.random.default_rng(7)
+    tokens = 256
+    k, v = (rng.integers(-127, 128, (tokens, dim)).astype(np.int8) for _ in range(2))
+    k[:, 5] = 0
+    q = rng.uniform(1, 2, (new, 1, dim)) * rng.choice([-1, 1], (new, 1, dim))
+    q = torch.from_numpy(q).bfloat16()
+    q = q * small
+    q[..., 5] = 1.5
+    q = q * row
+    Q = q.cuda().flatten(1)
+    dk = np.full(tokens // BLOCK, 0.01 / small / row, np.float32)
+    dv = np.full(tokens // BLOCK, 0.02, np.float32)
+    cache = make_cache(B, k, v, dk, dv)
+    Y, lse = B.bitnet_kv_attention(cache, Q, 1, ints([0, new]), ints([length]),
+                                   ints(np.arange(4))[None], new, scale=0.125, want_lse=True)
+    B.bitnet_sync_status()
+    check(Y, lse, expected(q.double().numpy(), k, v, dk, dv, 0.125, length, new))
