@@ -7,11 +7,13 @@
 //   y = (h * rinv) * g,  rinv = 1 / sqrt(sum h^2 / K + eps)   (each an IEEE fp32 operation)
 //   codes of y: absmax INT8 or absmean INT4, as act_quant_plain_kernel.
 // The norm reads the ROUNDED h: it is what the stream holds and what every later reader sees, so
-// one call gives what the addition followed by bitnet_act_quant_norm gives.
+// one call gives what the addition followed by bitnet_act_quant_norm gives.  One thing differs: a NaN
+// or an infinity of a row reaches its scale (and its codes are 0), so that products with the row are
+// NaN and not small plausible numbers.
 //
 // Bound by HBM: 6 bytes and the code an element, read once.  A row stays in the registers of its
 // threads between the addition and the codes (4 chunks of 8 values each, so K / 32 threads a row).
-// Measured on B200: 16383 x 4096 in 72 .. 75 us (6.2 .. 6.5 TB/s), 4096 x 2048 in 12 .. 14 us, one row
+// Measured on B200: 16383 x 4096 in 72 .. 76 us (6.2 .. 6.5 TB/s), 4096 x 2048 in 12 .. 14 us, one row
 // in the 3.4 us of a launch.  Rows above K = 32768 need more threads than a block has and are read
 // back: 4.2 TB/s at 33024 against 4.4 TB/s at 32768.
 #include "common.cuh"
@@ -28,6 +30,12 @@ __device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
     const float hi = __fadd_rn(__uint_as_float(a & 0xFFFF0000u), __uint_as_float(b & 0xFFFF0000u));
     uint32_t d;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {  // fmaxf would drop a NaN
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
     return d;
 }
 
@@ -151,24 +159,27 @@ __global__ void __launch_bounds__(1024)
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) sa += __shfl_xor_sync(0xFFFFFFFFu, sa, o);
         }
-        g = (float)fmax(sa / (double)K, 1e-5);
+        const double mean = sa / (double)K;
+        g = (float)(mean < 1e-5 ? 1e-5 : mean);  // keeps NaN
     } else {
-        float mx = 0.f;
+        float most = 0.f;
         each(rinv, [&](int, float2 (&y)[4]) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) mx = fmaxf(mx, fmaxf(fabsf(y[i].x), fabsf(y[i].y)));
+            for (int i = 0; i < 4; ++i) most = max_nan(most, max_nan(fabsf(y[i].x), fabsf(y[i].y)));
         });
-        // non-negative floats order like their bit patterns
-        uint32_t m = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(mx));
+        // non-negative floats order like their bit patterns, NaN above everything
+        uint32_t m = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most) & 0x7FFFFFFFu);
         if (warps > 1) {
-            float *red = reinterpret_cast<float *>(red_abs);
-            if (lane == 0) red[threadIdx.x >> 5] = __uint_as_float(m);
+            uint32_t *red = reinterpret_cast<uint32_t *>(red_abs);
+            if (lane == 0) red[threadIdx.x >> 5] = m;
             __syncthreads();
-            m = __reduce_max_sync(0xFFFFFFFFu, lane < warps ? __float_as_uint(red[warp0 + lane]) : 0u);
+            m = __reduce_max_sync(0xFFFFFFFFu, lane < warps ? red[warp0 + lane] : 0u);
         }
-        g = fmaxf(__uint_as_float(m), 1e-5f);
+        const float mx = __uint_as_float(m);
+        g = mx < 1e-5f ? 1e-5f : mx;
     }
     const float s = __fdiv_rn(Q, g);
+    const uint32_t keep = g <= 3.4028235e38f ? 0xFFFFFFFFu : 0u;  // codes of 0 beside a NaN or inf
     const float2 magic2 = make_float2(12582912.f, 12582912.f);  // 1.5 * 2^23: round to integer
     int sum = 0;
     each(rinv, [&](int c, float2 (&y)[4]) {
@@ -183,8 +194,8 @@ __global__ void __launch_bounds__(1024)
             f[2 * i] = __float_as_uint(u.x);
             f[2 * i + 1] = __float_as_uint(u.y);
         }
-        const uint32_t A = gather_low_bytes(f[0], f[1], f[2], f[3]);
-        const uint32_t B = gather_low_bytes(f[4], f[5], f[6], f[7]);
+        const uint32_t A = gather_low_bytes(f[0], f[1], f[2], f[3]) & keep;
+        const uint32_t B = gather_low_bytes(f[4], f[5], f[6], f[7]) & keep;
         sum = __dp4a((int)A, 0x01010101, sum);
         sum = __dp4a((int)B, 0x01010101, sum);
         if constexpr (BITS == 8)

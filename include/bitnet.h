@@ -161,7 +161,9 @@ int bitnet_act_quant_norm(const void *X_dev, int64_t M, int64_t K, const void *n
  * transform sits in front of Wo and Wdown, whose inputs are no residual streams).  Per token row:
  *   h = bf16_rn(x + r), stored;  then exactly bitnet_act_quant_norm on h.
  * The codes equal those of the two separate steps up to near-ties (the sum of squares is taken in
- * another fp32 order).
+ * another fp32 order).  A row with a NaN or infinite h, or a NaN or infinite y, gets a NaN or infinite
+ * scale, codes of 0 and a code sum of 0: every product with it is NaN.  (bitnet_act_quant and
+ * bitnet_act_quant_norm leave NaN out of the maximum or mean and give such a row arbitrary codes.)
  * X_dev   bf16 [M, K], the sub-layer's output.     R_dev  bf16 [M, K], the residual stream.
  * H_dev   out: bf16 [M, K], the new residual stream; may be X_dev or R_dev (in place), any other
  *         overlap is not allowed.

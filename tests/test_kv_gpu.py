@@ -166,6 +166,60 @@ def test_residual_norm_zero_and_nonfinite_rows_stay_apart(B):
     assert torch.isnan(H[2, 7]) and rowsum[3] == -127 * 512
 
 
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("K", [128, 2048, 33024])
+def test_residual_norm_nonfinite_rows_show(B, bits, K):
+    """A row with a NaN or an infinity gets codes of 0 and a scale that is NaN, so whatever is made of
+    it is NaN; the rows beside it (of the same block for small K) are what they are without it."""
+    rng = np.random.default_rng(K)
+    X, _ = bf16(rng.standard_normal((9, K)))
+    R, _ = bf16(rng.standard_normal((9, K)))
+    clean = B.bitnet_act_quant_residual_norm(X, R, None, 1e-5, bits)
+    X[1, K - 1] = float("nan")
+    R[3, 0] = float("inf")
+    X[4] = float("-inf")
+    X[6, 5], R[6, 5] = float("inf"), float("-inf")
+    bad = [1, 3, 4, 6]
+    good = [i for i in range(9) if i not in bad]
+    H, codes, scales, rowsum = B.bitnet_act_quant_residual_norm(X, R, None, 1e-5, bits)
+    B.bitnet_sync_status()
+    assert torch.equal(H.isnan() | H.isinf(), ~(X.float() + R.float()).isfinite())
+    assert torch.isnan(scales[bad]).all() and torch.all(codes[bad] == 0)
+    assert torch.all(rowsum[bad] == 0)
+    for got, want in zip((H, codes, scales, rowsum), clean):
+        assert torch.equal(got[good], want[good])
+    # a gain that is infinite where the row is not zero
+    G = torch.ones(K, dtype=torch.bfloat16, device="cuda")
+    G[7] = float("inf")
+    X, R = (t.clone() for t in (X, R))
+    X[0], R[0] = 0.0, 0.0                  # 0 * inf
+    X[2], R[2] = 1.0, 1.0
+    _, codes, scales, _ = B.bitnet_act_quant_residual_norm(X, R, G, 1e-5, bits)
+    assert torch.isnan(scales[0]) and torch.isinf(scales[2])
+    assert torch.all(codes[[0, 2]] == 0)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("M", [1, 6, 40, 300])
+def test_residual_norm_forward_of_nonfinite_rows_is_nan(B, bits, M):
+    """On every product kernel the output row of a NaN or infinite row is NaN, and no other."""
+    rng = np.random.default_rng(M)
+    K, N = 1024, 256
+    X, _ = bf16(rng.standard_normal((M, K)))
+    R, _ = bf16(rng.standard_normal((M, K)))
+    W = synth.to_torch_bf16(synth.latent_weights(N, K, seed=5)).cuda()
+    Wp, gamma = B.bitnet_quantize_pack_weights(W)
+    _, clean = B.bitnet_residual_norm_bitlinear_forward(X, R, None, 1e-5, Wp, gamma, bits)
+    bad = torch.zeros(M, dtype=torch.bool, device="cuda")
+    for row, value in ((0, "nan"), (M // 2, "inf"), (M - 1, "-inf")):
+        X[row, row] = float(value)
+        bad[row] = True
+    H, Y = B.bitnet_residual_norm_bitlinear_forward(X, R, None, 1e-5, Wp, gamma, bits)
+    B.bitnet_sync_status()
+    assert torch.isnan(Y[bad]).all()
+    assert torch.equal(Y[~bad], clean[~bad])
+
+
 # ----------------------------------------------------------------------------------------
 # cache: append and read back
 # ----------------------------------------------------------------------------------------
