@@ -144,12 +144,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int G = at.q_heads / a.kv_heads;
     // sequence s owns the units from first(s) * G / 256 + s on: room for the tiles of its rows
     auto begin = [&](int i) { return ((int64_t)__ldg(a.q_start + i) * G >> 8) + (int64_t)i; };
-    const int s = find_sequence(unit, a.batch, begin);
+    const int s = find_and_check(a, unit, tid == 0 && head == 0 && split == 0, begin,
+                                 [&](const KvSequence &) { return at.max_new; });
     const KvSequence q = kv_sequence(a, s);
-    if (!q.valid || q.count > at.max_new) {
-        if (tid == 0) record_status(a.status, BITNET_ERR_INVALID);
-        return;
-    }
+    if (!q.valid || q.count > at.max_new) return;  // nothing of it is read or written
     const int64_t tile = unit - begin(s);
     const int64_t all_rows = (int64_t)q.count * G;
     if (tile < 0 || tile * kRows >= all_rows) return;

@@ -41,12 +41,10 @@ struct Span {
 // False where this block has nothing to do.
 __device__ __forceinline__ bool find_span(const KvArgs &a, int shift, Span &x) {
     auto begin = [&](int s) { return (int64_t)(__ldg(a.q_start + s) >> shift) + 2 * (int64_t)s; };
-    x.s = find_sequence(blockIdx.x, a.batch, begin);
+    x.s = find_and_check(a, blockIdx.x, threadIdx.x == 0 && blockIdx.y == 0, begin,
+                         [](const KvSequence &q) { return q.length; });
     x.q = kv_sequence(a, x.s);
-    if (!x.q.valid || x.q.count > x.q.length) {  // nothing of such a sequence is read or written
-        if (threadIdx.x == 0) record_status(a.status, BITNET_ERR_INVALID);
-        return false;
-    }
+    if (!x.q.valid || x.q.count > x.q.length) return false;  // nothing of it is read or written
     const int64_t j = blockIdx.x - begin(x.s);
     if (j < 0 || x.q.count == 0) return false;
     const int p0 = x.q.length - x.q.count;

@@ -31,15 +31,41 @@ struct KvSequence {
     bool valid;
 };
 
-__device__ __forceinline__ KvSequence kv_sequence(const KvArgs &a, int s) {
+__device__ __forceinline__ KvSequence kv_sequence_of(const KvArgs &a, int b, int e, int length) {
     KvSequence q;
-    const int b = __ldg(a.q_start + s), e = __ldg(a.q_start + s + 1);
     q.first = b;
-    q.length = __ldg(a.kv_len + s);
+    q.length = length;
     q.valid = b >= 0 && e >= b && e <= a.tokens && q.length >= 0 &&
               (int64_t)q.length <= (int64_t)a.max_pages << a.page_shift;
     q.count = q.valid ? e - b : 0;
     return q;
+}
+
+__device__ __forceinline__ KvSequence kv_sequence(const KvArgs &a, int s) {
+    return kv_sequence_of(a, __ldg(a.q_start + s), __ldg(a.q_start + s + 1), __ldg(a.kv_len + s));
+}
+
+// The sequence of piece w of the work, found with find_sequence.  Where q_start goes back, a piece
+// may find another sequence than its own, so the pieces that find a sequence cannot answer for it
+// being reported: piece w also looks at sequence w (there are more pieces than sequences) if `look`,
+// and records one that is not valid or has more new tokens than most(sequence).  Its loads are asked
+// for in front of the search and looked at behind it.
+template <class F, class G>
+__device__ __forceinline__ int find_and_check(const KvArgs &a, int64_t w, bool look, F &&begin,
+                                              G &&most) {
+    int b = 0, e = 0, length = 0;
+    look = look && w < a.batch;
+    if (look) {
+        b = __ldg(a.q_start + w);
+        e = __ldg(a.q_start + w + 1);
+        length = __ldg(a.kv_len + w);
+    }
+    const int s = find_sequence(w, a.batch, begin);
+    if (look) {
+        const KvSequence q = kv_sequence_of(a, b, e, length);
+        if (!q.valid || q.count > most(q)) record_status(a.status, BITNET_ERR_INVALID);
+    }
+    return s;
 }
 
 // Page that holds `position` of sequence s, or -1 (recorded as an invalid argument); the entry of

@@ -456,7 +456,8 @@ typedef struct {
  * int32 on the device, so a captured graph can be replayed with other lengths and pages.
  *   q_start     [batch + 1]; rows q_start[s] .. q_start[s + 1] - 1 of the token matrices are the
  *               LAST tokens of sequence s.  Rows before q_start[0] and from q_start[batch] on
- *               belong to no sequence and stay as they were.
+ *               belong to no sequence and stay as they were.  0 <= q_start[0] <= q_start[1] ..
+ *               <= tokens.
  *   kv_len      [batch], each sequence's length with its new tokens (0 .. max_pages * page_tokens)
  *   page_table  [batch][max_pages]; the token at position p lies in page
  *               page_table[s][p / page_tokens].  Entries behind the length are not read.
@@ -465,6 +466,8 @@ typedef struct {
  * whose length leaves its page table, and a page number outside 0 .. num_pages - 1, make the next
  * bitnet_sync_status() return BITNET_ERR_INVALID.  Such a sequence is left out (its outputs stay
  * as they were); such a page is not written, and the tokens of it are not seen by the attention.
+ * Where q_start goes back, other sequences of the batch may be left out too, and rows that two of
+ * them claim are unspecified; rows and pages of no sequence still stay as they were.
  * tokens == 0 or batch == 0 does nothing.
  */
 typedef struct {

@@ -724,6 +724,89 @@ def test_invalid_sequences_and_pages_are_reported_and_left_out(B):
     B.bitnet_sync_status()
 
 
+def reported(B, call):
+    call()
+    with pytest.raises(B.BitnetError) as e:
+        B.bitnet_sync_status()
+    assert e.value.status == B.ERR_INVALID
+    B.bitnet_sync_status()   # cleared
+
+
+@pytest.mark.parametrize("q_start,tokens", [
+    ([0, 900, 3, 6], 6), ([43, 187, 0, 237], 400), ([141, 313, 205, 288], 400),
+    ([0, 200, 400, 0, 0, 10], 400), ([-5, 4, 8], 8), ([0, 4, 9], 8), ([0] * 40 + [300] + [7] * 30, 9),
+    (list(range(50)) + [20] + list(range(51, 70)), 70)])
+def test_q_start_that_goes_back_is_reported(B, q_start, tokens):
+    """Whichever blocks find the sequence: by every call, and rows that no valid sequence claims stay
+    as they were."""
+    heads, dim, page, group = 1, 64, 64, 4
+    n = len(q_start) - 1
+    cache = B.KvCache.empty(8 * n + 1, heads, dim, page, 16)
+    for t in (cache.k_codes, cache.v_codes, cache.k_scales, cache.v_scales):
+        t.zero_()
+    table = ints(np.arange(8 * n).reshape(n, 8))
+    meta = ints(q_start), ints([512] * n), table
+    claimed = torch.zeros(tokens, dtype=torch.bool, device="cuda")
+    for lo, hi in zip(q_start, q_start[1:]):
+        if 0 <= lo <= hi <= tokens:
+            claimed[lo:hi] = True
+    K = torch.ones((tokens, heads * dim), dtype=torch.bfloat16, device="cuda")
+    reported(B, lambda: B.bitnet_kv_cache_append(cache, K, K, *meta))
+    assert not cache.k_codes[8 * n].any() and not cache.v_scales[8 * n].any()
+    out = [torch.full_like(K, 7.0) for _ in range(2)]
+    reported(B, lambda: B.bitnet_kv_cache_read(cache, tokens, *meta, K=out[0], V=out[1]))
+    for t in out:
+        assert torch.all(t[~claimed] == 7)
+    Q = torch.ones((tokens, group * dim), dtype=torch.bfloat16, device="cuda")
+    for max_new in (8, 400):          # streaming (longer sequences are invalid there), prompts
+        Y = torch.full_like(Q, 7.0)
+        lse = torch.full((tokens, group), 7.0, device="cuda")
+        reported(B, lambda: B.bitnet_kv_attention(cache, Q, group, *meta, max_new, Y=Y, lse=lse))
+        assert torch.all(Y[~claimed] == 7) and torch.all(lse[~claimed] == 7)
+
+
+@pytest.mark.parametrize("new,group", [(2, 4), (8, 4), (20, 4), (70, 8)])
+def test_invalid_sequences_and_pages_of_both_attention_kernels(B, new, group):
+    rng = np.random.default_rng(new)
+    heads, dim, page = 2, 64, 16
+    b, cache, got = filled(B, rng, [new + 40, new + 33, new + 20], [new] * 3, heads, dim, page, 16)
+    q_heads = heads * group
+    Q, q = bf16(rng.standard_normal((b.tokens, q_heads * dim)))
+    start, length, table = b.device()
+    good, good_lse = B.bitnet_kv_attention(got, Q, q_heads, start, length, table, new, want_lse=True)
+
+    def call(*meta, **more):
+        Y = torch.full((b.tokens, q_heads * dim), 7.0, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((b.tokens, q_heads), 7.0, device="cuda")
+        reported(B, lambda: B.bitnet_kv_attention(got, Q, q_heads, *meta, new, Y=Y, lse=lse, **more))
+        return Y, lse
+
+    mid = slice(new, 2 * new)
+    for bad in (-1, 100000, 2**31 - 1):
+        Y, lse = call(start, ints([b.kv_len[0], bad, b.kv_len[2]]), table)
+        assert torch.all(Y[mid] == 7) and torch.all(lse[mid] == 7)
+        for rows in (slice(0, new), slice(2 * new, None)):
+            assert torch.equal(Y[rows], good[rows]) and torch.equal(lse[rows], good_lse[rows])
+    # a page that is not there: as if its tokens were not in the sequence
+    short = [b.kv_len[0], b.kv_len[1] - page, b.kv_len[2]]
+    without = b.table.copy()
+    without[1, :-1] = b.table[1, 1:]
+    y, l, tol_y, tol_l = ref.attention(cache, q.astype(np.float64).reshape(-1, q_heads, dim),
+                                       b.q_start, short, without, dim ** -0.5, False)
+    for wrong in (-1, b.pages, 2**31 - 1):
+        bad = b.table.copy()
+        bad[1, 0] = wrong
+        Y, lse = call(start, length, ints(bad), causal=False)
+        got_y = Y.float().cpu().numpy().reshape(y.shape)
+        assert np.all(np.abs(got_y - y) <= BF16_HALF * np.abs(y) + tol_y * (1 + BF16_HALF))
+        assert np.all(np.abs(lse.cpu().numpy() - l) <= tol_l)
+        # a sequence without any page sees nothing
+        bad[1, :] = wrong
+        Y, lse = call(start, length, ints(bad))
+        assert torch.all(Y[mid] == 0) and torch.all(lse[mid] == -float("inf"))
+        assert torch.equal(Y[:new], good[:new]) and torch.equal(Y[2 * new:], good[2 * new:])
+
+
 def test_empty_calls_do_nothing(B):
     rng = np.random.default_rng(1)
     b, cache, got = filled(B, rng, [5], [1], 1, 64, 16, 16)
