@@ -167,6 +167,34 @@ __device__ __forceinline__ void pdl_launch_dependents() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// Loads of what the kernel in front wrote, for kernels that are launched programmatically.  __ldg, or
+// a plain load through a const __restrict__ pointer, is a load of data that nothing writes while the
+// kernel runs: it may be moved in front of pdl_wait() and may be answered by a stale line of the L1
+// (seen on B200: a product that got the codes of the call before, in nearly every replay of a
+// graph whose calls share a workspace).  These are ordinary loads in program order.
+__device__ __forceinline__ uint4 ld_written_v4(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 ld_written_v2(const void *p) {
+    uint2 v;
+    asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t ld_written(const void *p) {
+    uint32_t v;
+    asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ int ld_written(const int32_t *p) {
+    return (int)ld_written(static_cast<const void *>(p));
+}
+__device__ __forceinline__ float ld_written(const float *p) {
+    return __uint_as_float(ld_written(static_cast<const void *>(p)));
+}
+
 // ------------------------------------------------------------------------------------------
 // TMA (bulk tensor copies).  No multicast form is used anywhere in this library.
 // ------------------------------------------------------------------------------------------

@@ -343,7 +343,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(num_threads<BITS>(),
         const int quad = warp & 3;                    // tensor-memory lanes = features
         const int eh = (warp - WARP_EPI) >> 2;        // tokens 128 eh .. +127 of the tile
         const uint32_t t_lane = tmem + ((uint32_t)(quad * 32) << 16);
-        const float gamma = *gamma_ptr;
+        const float gamma = ld_written(gamma_ptr);
         constexpr int CHUNKS = BT / 2 / 32;
         float2 *tok = reinterpret_cast<float2 *>(smem + OFF_TOK) + (warp - WARP_EPI) * (BT / 2);
         // |sum_k q c| <= 128 K (INT8) or 8 K (INT4): below 2^22 the exact FMA-pipe conversion
@@ -359,8 +359,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(num_threads<BITS>(),
 #pragma unroll
             for (int q = 0; q < CHUNKS; ++q) {
                 const int mj = mt * BT + eh * (BT / 2) + q * 32 + lane;
-                tok[q * 32 + lane] = make_float2(mj < M ? scales[mj] * gamma : 0.f,
-                                                 __int_as_float(mj < M ? rowsum[mj] : 0));
+                tok[q * 32 + lane] = make_float2(mj < M ? ld_written(scales + mj) * gamma : 0.f,
+                                                 __int_as_float(mj < M ? ld_written(rowsum + mj) : 0));
             }
             __syncwarp();
             if (!warp_wait(&bar->acc_full, (uint32_t)t & 1, status, lane)) break;

@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         // ------------------------------------------------------------------ epilogue
         // unit = (token m, 8 consecutive features); CTA `rank` takes every S-th group of 128
         pdl_wait();  // scales, code sums and Y belong to the stream order (returns at once here)
-        const float gamma = *gamma_ptr;
+        const float gamma = ld_written(gamma_ptr);
         const uint32_t red_addr = smem_addr(wring);
         const int units = M * (FEAT / 8);
         for (int u = rank * 128 + (int)threadIdx.x; u < units; u += S * 128) {
@@ -396,11 +396,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 a[0] += (int)x0.x; a[1] += (int)x0.y; a[2] += (int)x0.z; a[3] += (int)x0.w;
                 a[4] += (int)x1.x; a[5] += (int)x1.y; a[6] += (int)x1.z; a[7] += (int)x1.w;
             }
-            const int rs = rowsum[m];
+            const int rs = ld_written(rowsum + m);
 #pragma unroll
             for (int i = 0; i < 8; ++i) a[i] -= rs;
             if constexpr (MODE == OUT_SWIGLU) {
-                const float sc = scales[m] * gamma;
+                const float sc = ld_written(scales + m) * gamma;
                 uint32_t pk[2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     dst[1] = make_int4(a[4], a[5], a[6], a[7]);
                 }
                 if (Y) {
-                    const float sc = scales[m] * gamma;
+                    const float sc = ld_written(scales + m) * gamma;
                     uint32_t pk[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {

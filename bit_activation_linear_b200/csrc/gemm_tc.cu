@@ -373,7 +373,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         const int half = (warp - WARP_EPI) >> 2;   // features 128*half .. 128*half+127
         const uint32_t t_lane = tmem + ((uint32_t)(wq * 32) << 16);
         uint8_t *ybox = sy + (size_t)(warp - WARP_EPI) * Y_BOX_BYTES;
-        const float gamma = *gamma_ptr;
+        const float gamma = ld_written(gamma_ptr);
         for (int t = 0; t < my_units; ++t) {
             int tile, kb, ke;
             unit(t, tile, kb, ke);
@@ -382,8 +382,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
             const int ab = t & 1;
             const int64_t m = (int64_t)mt * BM + (int)rank * HM + wq * 32 + lane;
             const bool m_ok = m < M;
-            const float sc = m_ok ? scales[m] * gamma : 0.f;
-            const int rs = m_ok ? rowsum[m] : 0;
+            const float sc = m_ok ? ld_written(scales + m) * gamma : 0.f;
+            const int rs = m_ok ? ld_written(rowsum + m) : 0;
             if (!warp_wait(&bar->acc_full[ab], (uint32_t)(t >> 1) & 1, status, lane)) break;
             tc_fence_after();
 #pragma unroll 1

@@ -49,6 +49,14 @@ __device__ __forceinline__ void gemv_finish(const int (&acc)[R][T], int (*red)[R
                                             __nv_bfloat16 *__restrict__ Y) {
     static_assert(ACT != 2 || R % 2 == 0, "SwiGLU needs the gate and up rows in one group");
     const int warp = threadIdx.x >> 5;
+    // lane r*T + t (p*T + t) writes token t: its scale and code sum, asked for in front of the sums
+    const int mine = lane % T;
+    float sc = 0.f;
+    int rs = 0;
+    if (active && mine < M && warp % KS == 0) {
+        sc = ld_written(scales + mine) * ld_written(gamma_ptr);
+        rs = ld_written(rowsum + mine);
+    }
     int sums[R][T];  // full sums, the same in every lane
 #pragma unroll
     for (int r = 0; r < R; ++r)
@@ -78,17 +86,15 @@ __device__ __forceinline__ void gemv_finish(const int (&acc)[R][T], int (*red)[R
             }
     }
     if (!active) return;
-    const float gamma = *gamma_ptr;
 #pragma unroll
     for (int t = 0; t < T; ++t) {
         if (t >= M) break;
-        const float sc = scales[t] * gamma;
         if constexpr (ACT == 2) {
 #pragma unroll
             for (int p = 0; p < R / 2; ++p) {
                 if (lane == p * T + t && n0 + 2 * p + 1 < N) {
-                    const float g = (float)(sums[2 * p][t] - rowsum[t]) * sc;
-                    const float u = (float)(sums[2 * p + 1][t] - rowsum[t]) * sc;
+                    const float g = (float)(sums[2 * p][t] - rs) * sc;
+                    const float u = (float)(sums[2 * p + 1][t] - rs) * sc;
                     Y[(int64_t)t * (N / 2) + n0 / 2 + p] =
                         __float2bfloat16_rn(__fdiv_rn(g, 1.f + expf(-g)) * u);
                 }
@@ -98,7 +104,7 @@ __device__ __forceinline__ void gemv_finish(const int (&acc)[R][T], int (*red)[R
             for (int r = 0; r < R; ++r) {
                 const int n = n0 + r;
                 if (lane == r * T + t && n < N) {
-                    const int a = sums[r][t] - rowsum[t];
+                    const int a = sums[r][t] - rs;
                     if (acc_out) acc_out[(int64_t)t * N + n] = a;
                     if (Y) {
                         float y = (float)a * sc;
@@ -173,46 +179,65 @@ __global__ void __launch_bounds__(kGemvWarps * 32)
         // codes started, so they are loaded before waiting for that kernel (programmatic
         // dependent launch); the codes, scales and code sums are always read after the wait.
         if (early_weights && b0 == 0) pdl_wait();
+        // codes k0 .. k0+15 of every token as four words of four int8 (word p = k0+4p .. +3), G steps
+        // asked for at once: one at a time each waits for the one before (8192 x 2048 INT4, one token:
+        // 15.6 us, 10.9 with eight; 2048 x 2048, eight tokens: 7.5 us, 6.4 with two).  Four rows of
+        // eight tokens leave no registers for a second step (8192 x 8192: 25.7 us, 30.5 with two).
+        constexpr int G = T < 8 ? 8 / T : R <= 2 ? 2 : 1;
 #pragma unroll
-        for (int j = 0; j < S; ++j) {
-            if (b0 + j >= mine) break;
-            const int k0 = 512 * (ks + KS * (b0 + j)) + 16 * lane;
-            const bool k_in = k0 < K;  // lanes past the end of a partial step add zero
-            // codes k0 .. k0+15 of every token as four words of four int8 (word p = k0+4p .. +3)
-            uint32_t xs[T][4];
+        for (int j0 = 0; j0 < S; j0 += G) {
+            if (b0 + j0 >= mine) break;
+            uint32_t xg[G][T][4];
 #pragma unroll
-            for (int t = 0; t < T; ++t) {
-                uint32_t *x = xs[t];
-                if (!k_in || t >= M) {
-                    x[0] = x[1] = x[2] = x[3] = 0u;
-                } else if constexpr (BITS == 8) {
-                    const uint4 v = __ldg(reinterpret_cast<const uint4 *>(codes + (int64_t)t * K + k0));
-                    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-                } else {
-                    // nibble storage: each word holds codes k..k+3 (low nibbles), k+4..k+7 (high)
-                    const uint2 v =
-                        __ldg(reinterpret_cast<const uint2 *>(codes + (int64_t)t * (K / 2) + k0 / 2));
-                    x[0] = sext_nibbles(v.x & 0x0F0F0F0Fu);
-                    x[1] = sext_nibbles((v.x >> 4) & 0x0F0F0F0Fu);
-                    x[2] = sext_nibbles(v.y & 0x0F0F0F0Fu);
-                    x[3] = sext_nibbles((v.y >> 4) & 0x0F0F0F0Fu);
-                }
-            }
-            // packed word: weight k0 + 4p + j at bits 8j + 2p, as offset codes u = q + 1
+            for (int g = 0; g < G; ++g) {
+                const int k0 = 512 * (ks + KS * (b0 + j0 + g)) + 16 * lane;
+                const bool k_in = b0 + j0 + g < mine && k0 < K;  // lanes past the end add zero
 #pragma unroll
-            for (int r = 0; r < R; ++r)
-#pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    if constexpr (FIELD_SUMS) {
-                        const uint32_t um = w[r][j] & (0x03030303u << (2 * p));
-#pragma unroll
-                        for (int t = 0; t < T; ++t) fs[r][t][p] = dp4a_us(um, xs[t][p], fs[r][t][p]);
+                for (int t = 0; t < T; ++t) {
+                    uint32_t *x = xg[g][t];
+                    if (!k_in || t >= M) {
+                        x[0] = x[1] = x[2] = x[3] = 0u;
+                    } else if constexpr (BITS == 8) {
+                        const uint4 v = ld_written_v4(codes + (int64_t)t * K + k0);
+                        x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
                     } else {
-                        const int u = (int)((w[r][j] >> (2 * p)) & 0x03030303u);
-#pragma unroll
-                        for (int t = 0; t < T; ++t) acc[r][t] = __dp4a(u, (int)xs[t][p], acc[r][t]);
+                        // nibble storage: a word holds codes k..k+3 (low nibbles), k+4..k+7 (high)
+                        const uint2 v = ld_written_v2(codes + (int64_t)t * (K / 2) + k0 / 2);
+                        x[0] = v.x; x[1] = v.y;
                     }
                 }
+            }
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const int j = j0 + g;
+                if (b0 + j >= mine) break;
+                uint32_t (&xs)[T][4] = xg[g];
+                if constexpr (BITS == 4) {
+#pragma unroll
+                    for (int t = 0; t < T; ++t) {
+                        const uint32_t x = xs[t][0], y = xs[t][1];
+                        xs[t][0] = sext_nibbles(x & 0x0F0F0F0Fu);
+                        xs[t][1] = sext_nibbles((x >> 4) & 0x0F0F0F0Fu);
+                        xs[t][2] = sext_nibbles(y & 0x0F0F0F0Fu);
+                        xs[t][3] = sext_nibbles((y >> 4) & 0x0F0F0F0Fu);
+                    }
+                }
+                // packed word: weight k0 + 4p + j at bits 8j + 2p, as offset codes u = q + 1
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        if constexpr (FIELD_SUMS) {
+                            const uint32_t um = w[r][j] & (0x03030303u << (2 * p));
+#pragma unroll
+                            for (int t = 0; t < T; ++t) fs[r][t][p] = dp4a_us(um, xs[t][p], fs[r][t][p]);
+                        } else {
+                            const int u = (int)((w[r][j] >> (2 * p)) & 0x03030303u);
+#pragma unroll
+                            for (int t = 0; t < T; ++t) acc[r][t] = __dp4a(u, (int)xs[t][p], acc[r][t]);
+                        }
+                    }
+            }
         }
         if constexpr (FIELD_SUMS) {
 #pragma unroll
@@ -356,36 +381,48 @@ __global__ void __launch_bounds__(kGemvWarps * 32)
                               : 0u;  // byte 0 decodes to u = 0: adds nothing
         }
         if (early_weights && b0 == 0) pdl_wait();
+        // codes k0 + 4p .. +3 of every token (K % 4 == 0: a group is wholly in or out), G steps asked
+        // for at once
+        constexpr int G = T >= 4 ? 1 : 4 / T;
 #pragma unroll
-        for (int j = 0; j < S; ++j) {
-            if (b0 + j >= mine) break;
-            const int k0 = 20 * (32 * (ks + KS * (b0 + j)) + lane);
-            // codes k0 + 4p .. +3 of every token (K % 4 == 0: a group is wholly in or out)
-            uint32_t xs[T][5];
+        for (int j0 = 0; j0 < S; j0 += G) {
+            if (b0 + j0 >= mine) break;
+            uint32_t xg[G][T][5];
 #pragma unroll
-            for (int t = 0; t < T; ++t)
+            for (int g = 0; g < G; ++g) {
+                const int k0 = 20 * (32 * (ks + KS * (b0 + j0 + g)) + lane);
+                const bool k_in = b0 + j0 + g < mine;
 #pragma unroll
-                for (int p = 0; p < 5; ++p)
-                    xs[t][p] = (t < M && k0 + 4 * p < K)
-                                   ? __ldg(reinterpret_cast<const uint32_t *>(
-                                         codes + (int64_t)t * K + k0 + 4 * p))
-                                   : 0u;
+                for (int t = 0; t < T; ++t)
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const uint32_t v = w[r][j];
-                const unsigned long long L0 = digits[v & 0xFFu], L1 = digits[(v >> 8) & 0xFFu],
-                                         L2 = digits[(v >> 16) & 0xFFu], L3 = digits[v >> 24];
-                // offset codes of weights k0 .. k0+19, four per word in k order
-                const uint32_t u[5] = {(uint32_t)L0,
-                                       (uint32_t)(L0 >> 32) | (uint32_t)(L1 << 8),
-                                       (uint32_t)(L1 >> 24) | (uint32_t)(L2 << 16),
-                                       (uint32_t)(L2 >> 16) | (uint32_t)(L3 << 24),
-                                       (uint32_t)(L3 >> 8)};
+                    for (int p = 0; p < 5; ++p)
+                        xg[g][t][p] = (k_in && t < M && k0 + 4 * p < K)
+                                          ? ld_written(static_cast<const void *>(
+                                                codes + (int64_t)t * K + k0 + 4 * p))
+                                          : 0u;
+            }
 #pragma unroll
-                for (int p = 0; p < 5; ++p)
+            for (int g = 0; g < G; ++g) {
+                const int j = j0 + g;
+                if (b0 + j >= mine) break;
+                const uint32_t (&xs)[T][5] = xg[g];
 #pragma unroll
-                    for (int t = 0; t < T; ++t)
-                        acc[r][t] = __dp4a((int)u[p], (int)xs[t][p], acc[r][t]);
+                for (int r = 0; r < R; ++r) {
+                    const uint32_t v = w[r][j];
+                    const unsigned long long L0 = digits[v & 0xFFu], L1 = digits[(v >> 8) & 0xFFu],
+                                             L2 = digits[(v >> 16) & 0xFFu], L3 = digits[v >> 24];
+                    // offset codes of weights k0 .. k0+19, four per word in k order
+                    const uint32_t u[5] = {(uint32_t)L0,
+                                           (uint32_t)(L0 >> 32) | (uint32_t)(L1 << 8),
+                                           (uint32_t)(L1 >> 24) | (uint32_t)(L2 << 16),
+                                           (uint32_t)(L2 >> 16) | (uint32_t)(L3 << 24),
+                                           (uint32_t)(L3 >> 8)};
+#pragma unroll
+                    for (int p = 0; p < 5; ++p)
+#pragma unroll
+                        for (int t = 0; t < T; ++t)
+                            acc[r][t] = __dp4a((int)u[p], (int)xs[t][p], acc[r][t]);
+                }
             }
         }
     }
