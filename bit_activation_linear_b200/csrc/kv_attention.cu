@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1)
         const int first = c0 + warp;
         const int count = real > first ? (real - first + kWarps - 1) / kWarps : 0;
         const int32_t *table = a.page_table + (int64_t)s * a.max_pages;
-        int page = count > 0 ? __ldg(table + (first * kChunk >> a.page_shift)) : 0;  // of the next
+        int page = count > 0 ? table[first * kChunk >> a.page_shift] : 0;  // of the next
         int bring_pos = first * kChunk, left = count;                                 // chunk
         uint32_t bring_to = ring;
         auto bring = [&]() {
@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1)
                 --left;
                 bring_pos += kWarps * kChunk;
                 bring_to = bring_to == ring + (kStages - 1) * STAGE ? ring : bring_to + STAGE;
-                if (left > 0) page = __ldg(table + (bring_pos >> a.page_shift));
+                if (left > 0) page = table[bring_pos >> a.page_shift];
             }
             cp_async_commit();
         };
@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1)
 #pragma unroll
                 for (int j = 0; j < KW / 4; ++j) {
                     const uint4 *v = reinterpret_cast<const uint4 *>(src + 32 * (t + 4 * j));
-                    const uint4 x = __ldg(v), y = __ldg(v + 1);
+                    const uint4 x = v[0], y = v[1];
                     w[4 * j] = make_uint2(x.x, x.y);
                     w[4 * j + 1] = make_uint2(x.z, x.w);
                     w[4 * j + 2] = make_uint2(y.x, y.y);

@@ -41,8 +41,10 @@ __device__ __forceinline__ KvSequence kv_sequence_of(const KvArgs &a, int b, int
     return q;
 }
 
+// (No __ldg here, in kv_page_entry and in the streaming kernel, which is launched programmatically: it
+// runs, up to its pdl_wait(), beside the kernel that may be writing these; see ld_written in common.cuh.)
 __device__ __forceinline__ KvSequence kv_sequence(const KvArgs &a, int s) {
-    return kv_sequence_of(a, __ldg(a.q_start + s), __ldg(a.q_start + s + 1), __ldg(a.kv_len + s));
+    return kv_sequence_of(a, a.q_start[s], a.q_start[s + 1], a.kv_len[s]);
 }
 
 // The sequence of piece w of the work, found with find_sequence.  Where q_start goes back, a piece
@@ -71,7 +73,7 @@ __device__ __forceinline__ int find_and_check(const KvArgs &a, int64_t w, bool l
 // Page that holds `position` of sequence s, or -1 (recorded as an invalid argument); the entry of
 // the page table and its check apart, for kernels that ask for it ahead of its use.
 __device__ __forceinline__ int kv_page_entry(const KvArgs &a, int s, int position) {
-    return __ldg(a.page_table + (int64_t)s * a.max_pages + (position >> a.page_shift));
+    return a.page_table[(int64_t)s * a.max_pages + (position >> a.page_shift)];
 }
 __device__ __forceinline__ int kv_page_checked(const KvArgs &a, int page) {
     if (page < 0 || page >= a.num_pages) {

@@ -914,6 +914,50 @@ def test_chains_of_calls_that_nothing_waits_between(B, own_stream):
     assert all(torch.equal(x, y) for x, y in zip(*results))
 
 
+@pytest.mark.parametrize("M", [8, 32, 64])
+def test_attention_right_behind_the_product_that_makes_its_queries(B, M):
+    """Products and attention on the same buffers in turn, in a replayed graph and with nothing
+    between them: the attention is launched while the product still runs, and reads its queries."""
+    heads, dim, group = 2, 64, 4
+    rng = np.random.default_rng(M)
+    b, cache, got = filled(B, rng, [400, 100], [M // 2, M // 2], heads, dim, 64, 16)
+    meta = b.device()
+    width, K = heads * group * dim, 2048
+    W = synth.to_torch_bf16(synth.latent_weights(width, K, seed=3)).cuda()
+    Wp, gamma = B.bitnet_quantize_pack_weights(W)
+    X = torch.stack([bf16(rng.standard_normal((M, K)))[0] for _ in range(8)])
+    want = []
+    for x in X:
+        Q = B.bitnet_bitlinear_forward(x, Wp, gamma, 8)
+        torch.cuda.synchronize()
+        want.append(B.bitnet_kv_attention(got, Q, heads * group, *meta, M // 2, want_lse=True))
+        torch.cuda.synchronize()
+    Q = torch.empty((M, width), dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(B.bitnet_workspace_bytes(M, K, width, 8), dtype=torch.uint8, device="cuda")
+    B.bitnet_bitlinear_forward(X[0], Wp, gamma, 8, Y=Q, ws=ws)
+    outs = []
+
+    def chain():
+        outs.clear()
+        for x in X:
+            B.bitnet_bitlinear_forward(x, Wp, gamma, 8, Y=Q, ws=ws)
+            outs.append(B.bitnet_kv_attention(got, Q, heads * group, *meta, M // 2, want_lse=True))
+
+    chain()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chain()
+    for _ in range(20):
+        for o in outs:
+            o[0].zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            assert torch.equal(o[0], w[0]) and torch.equal(o[1], w[1])
+    B.bitnet_sync_status()
+
+
 def test_a_layer_step_residual_norm_qkv_cache_attention(B):
     """The operators one after the other as a decoder layer runs them: residual norm and Q/K/V
     product, cache write, attention, H-BitLinear output projection; a prompt, then single tokens,
