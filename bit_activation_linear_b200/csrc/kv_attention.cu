@@ -56,7 +56,6 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kStages = 3;
-constexpr uint32_t kNoPage = 0xFFFFFFFFu;  // a step (a NaN that no product gives)
 constexpr float kTop = 7.f;     // log2 of where a moved reference puts the largest weight, and of
 constexpr float kLimit = 15.f;  // the weight above which it moves
 constexpr int kMinChunks = 32;  // shorter ranges do not repay the second launch (about 4 us)
@@ -227,7 +226,9 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1)
         int page = count > 0 ? table[first * kChunk >> a.page_shift] : 0;  // of the next
         int bring_pos = first * kChunk, left = count;                                 // chunk
         uint32_t bring_to = ring;
+        uint32_t no_page = 0;  // bit k: the chunk that was asked for k calls ago has no page
         auto bring = [&]() {
+            no_page <<= 1;
             if (left > 0) {
                 if ((uint32_t)page < (uint32_t)a.num_pages) {
                     const int in_page = bring_pos & ((1 << a.page_shift) - 1);
@@ -245,11 +246,8 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1)
                         cp_async4(bring_to + 2 * CB + 4 * lane,
                                   my_scales + (tile << scale_shift) + (in_page >> a.block_shift));
                 } else {
-                    // tokens of no page weigh nothing: a step of K that is marked
                     record_status(a.status, BITNET_ERR_INVALID);
-                    if (lane < 2)
-                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(bring_to + 2 * CB + 4 * lane),
-                                     "r"(kNoPage) : "memory");
+                    no_page |= 1;
                 }
                 --left;
                 bring_pos += kWarps * kChunk;
@@ -329,8 +327,8 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 2 : 1)
             bring();
             cp_async_wait<kStages - 1>();
             __syncwarp();
-            const uint2 step2 = lds64(stage + 2 * CB);
-            if (step2.x != kNoPage) {
+            if (!(no_page >> (kStages - 1) & 1)) {  // tokens of no page weigh nothing
+                const uint2 step2 = lds64(stage + 2 * CB);
                 const float dk = __uint_as_float(step2.x), dv = v_step(__uint_as_float(step2.y));
                 float sc[NT][4];
 #pragma unroll

@@ -481,6 +481,25 @@ def test_attention_nonfinite_values_reach_their_rows_only(B, new):
     B.bitnet_sync_status()
 
 
+@pytest.mark.parametrize("bits", [0xFFFFFFFF, 0x7FFFFFFF, 0x7FC00000, 0xFFC00000, 0x7F800001])
+@pytest.mark.parametrize("new", [1, 9, 40])
+def test_attention_shows_any_nan_step(B, new, bits):
+    """Whatever the NaN's bits: the rows of its head that see the block are NaN, and no others."""
+    rng = np.random.default_rng(2)
+    heads, dim = 2, 64
+    b, cache, got = filled(B, rng, [200], [new], heads, dim, 64, 16)
+    Q, _ = bf16(rng.standard_normal((new, 2 * heads * dim)))
+    clean, _ = B.bitnet_kv_attention(got, Q, 2 * heads, *b.device(), new)
+    for steps in (got.k_scales, got.v_scales):
+        keep = steps.clone()
+        steps.view(torch.int32)[int(b.table[0, 0]), 1, 2] = bits - 2**32 if bits >= 2**31 else bits
+        Y, lse = B.bitnet_kv_attention(got, Q, 2 * heads, *b.device(), new, want_lse=True)
+        B.bitnet_sync_status()
+        assert torch.isnan(Y[:, 2 * dim:]).all() and torch.isnan(lse[:, 2:]).all()
+        assert torch.equal(Y[:, :2 * dim], clean[:, :2 * dim])
+        steps.copy_(keep)
+
+
 @pytest.mark.parametrize("q_scale,k_scale", [(1e-20, 1e10), (1e20, 1e-20), (300.0, 1.0),
                                              (1e-3, 1e-6)])
 @pytest.mark.parametrize("new", [1, 30])
