@@ -889,7 +889,7 @@ def _rows(t, name: str, width: int, tokens, dev: int):
             raise ValueError(f"the columns of {name} must be contiguous")
     elif len(shape) == 3:
         cols = shape[1] * shape[2]
-        if not t.is_contiguous() and (stride[2] != 1 or stride[1] != shape[2]):
+        if not t.is_contiguous() and (stride[2] != 1 or shape[1] > 1 and stride[1] != shape[2]):
             raise ValueError(f"the heads of a row of {name} must lie one after the other")
     else:
         raise ValueError(f"{name} must have 2 or 3 dimensions")

@@ -165,3 +165,20 @@ def test_binding_refuses_what_the_library_cannot_see(B):
         B._rows(x, "Q", 256, None, 0)
     with pytest.raises(TypeError):
         B._rows([1], "Q", 256, None, 0)
+
+
+def test_rows_of_one_head_in_any_layout(B):
+    """[tokens, heads, head_dim] with one head (or one token): the distance of the heads (of the rows)
+    means nothing then and may be anything."""
+    wide = torch.zeros((1, 6, 256), dtype=torch.bfloat16)
+    one_head = wide[:, :, 64:128].transpose(0, 1)
+    assert one_head.shape == (6, 1, 64) and not one_head.is_contiguous()
+    assert B._rows(one_head, "K", 64, 6, -1) == (one_head.data_ptr(), 256)
+    one_token = torch.zeros((4, 2, 64), dtype=torch.bfloat16)[2:3]
+    assert B._rows(one_token, "K", 128, 1, -1) == (one_token.data_ptr(), 128)
+    heads = torch.zeros((6, 4, 64), dtype=torch.bfloat16)
+    assert B._rows(heads[:, 1:3], "K", 128, 6, -1) == (heads.data_ptr() + 128, 256)
+    with pytest.raises(ValueError, match="one after the other"):
+        B._rows(heads[:, ::2], "K", 128, 6, -1)
+    with pytest.raises(ValueError, match="one after the other"):
+        B._rows(heads[:, :, ::2], "K", 128, 6, -1)
