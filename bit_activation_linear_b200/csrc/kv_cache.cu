@@ -23,9 +23,10 @@ namespace bitnet {
 namespace {
 
 // A block takes a span of positions of one sequence (64 or a longer scale block where there are many,
-// else less: span_grid), for several heads, K and V: finding the sequence and its pages costs a dozen dependent loads and integer
-// divisions, which a warp a head would spend more time on than on its few KB.  Its warps go over the
-// (K or V, head) pairs, neighbours at neighbouring heads, so that together they read whole rows.
+// else less: span_grid), for several heads, K and V: finding the sequence and its pages costs a dozen
+// dependent loads and integer divisions, which a warp a head would spend more time on than on its few
+// KB.  Its warps go over the (K or V, head) pairs, neighbours at neighbouring heads, so that together
+// they read whole rows.
 // Sequence s owns the spans from first(s) / span + 2 s on: that is non-decreasing, leaves room for
 // the spans that n tokens can touch (n / span + 2), and needs no prefix sum.
 constexpr int kWarps = 8;
@@ -177,8 +178,6 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
     }
 }
 
-// Reads back a sequence's last tokens, 16 positions of one head at a time.  A scale block is at
-// least 16 tokens, so the 16 share a step.
 // Four codes as two pairs of bf16 values.  The byte c xor 0x80 under 0x4B0000 is the float 2^23 + 128
 // + c: one byte permutation and an exact subtraction (int to float conversions, 16 a clock and SM,
 // kept half of the reading time busy).
@@ -191,6 +190,8 @@ __device__ __forceinline__ uint2 values4(uint32_t codes, float d) {
     return make_uint2(bf16x2_of(v[0], v[1]), bf16x2_of(v[2], v[3]));
 }
 
+// Reads back a sequence's last tokens, 16 positions of one head at a time.  A scale block is at
+// least 16 tokens, so the 16 share a step.
 template <int D>
 __global__ void __launch_bounds__(32 * kWarps, 6)
     kv_read_kernel(KvArgs a, uint8_t *__restrict__ K, int64_t ldk, uint8_t *__restrict__ V,

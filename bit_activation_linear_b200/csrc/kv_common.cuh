@@ -102,6 +102,8 @@ __device__ __forceinline__ int64_t kv_scale_at(const KvArgs &a, int page, int he
 // What the attention kernels share
 // ------------------------------------------------------------------------------------------
 constexpr int kChunk = 16;      // tokens: a scale block is a whole number of chunks
+// The SMs that splits are made for: a constant, because the workspace query answers without a device
+// and the launch has to come to the same split.
 constexpr int kSms = 148;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNothing = -3.0e38f;  // the reference of a row that has seen nothing

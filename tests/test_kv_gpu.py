@@ -900,6 +900,45 @@ def test_attention_on_two_streams_and_in_replayed_graphs(B, new):
     B.bitnet_sync_status()
 
 
+def test_calls_from_several_host_threads(B):
+    """A thread a stream, each with its own cache: writes, reads back and attention of both kernels and
+    head sizes at once give what they give one after the other."""
+    import threading
+
+    def work(dim, seed, stream, out):
+        with torch.cuda.stream(stream):
+            gen = torch.Generator(device="cuda").manual_seed(seed)
+
+            def rand(*shape):
+                return torch.randn(shape, generator=gen, device="cuda").bfloat16()
+
+            cache = B.KvCache.empty(20, 2, dim)
+            table = torch.arange(20, dtype=torch.int32, device="cuda")[None]
+            meta = ints([0, 700]), ints([700]), table
+            B.bitnet_kv_cache_append(cache, rand(700, 2 * dim), rand(700, 2 * dim), *meta)
+            out += B.bitnet_kv_cache_read(cache, 700, *meta)
+            for new, heads in ((1, 4), (5, 8), (80, 4)):
+                for _ in range(10):
+                    out += B.bitnet_kv_attention(cache, rand(new, heads * dim), heads, ints([0, new]),
+                                                 ints([700]), table, new, want_lse=True)
+            stream.synchronize()
+
+    jobs = [(dim, seed, torch.cuda.Stream()) for dim in (64, 128) for seed in range(4)]
+    want = []
+    for job in jobs:
+        want.append([])
+        work(*job, want[-1])
+    got = [[] for _ in jobs]
+    threads = [threading.Thread(target=work, args=(*job, out)) for job, out in zip(jobs, got)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for a, b in zip(got, want):
+        assert len(a) == len(b) and all(torch.equal(x, y) for x, y in zip(a, b))
+    B.bitnet_sync_status()
+
+
 @pytest.mark.parametrize("own_stream", [False, True])
 def test_chains_of_calls_that_nothing_waits_between(B, own_stream):
     """Writes and attention of growing sequences, one call after the other, give what they give with
