@@ -533,7 +533,7 @@ static cudaError_t launch_fwht_t(const void *X, int64_t M, const NormArgs &nrm, 
                                  float *scales, int32_t *rowsum, float *zout, int *status,
                                  cudaStream_t stream) {
     auto kern = fwht_quant_kernel<P, BITS, ZOUT, NORM, ABSMEAN>;
-    static bool configured[64] = {};
+    static std::atomic<bool> configured[64];
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 0 && dev < 64 && !configured[dev]) {
@@ -542,15 +542,17 @@ static cudaError_t launch_fwht_t(const void *X, int64_t M, const NormArgs &nrm, 
         if (e != cudaSuccess) return e;
         configured[dev] = true;
     }
-    static int per_sm[64] = {};
-    static int num_sms[64] = {};
-    if (dev >= 0 && dev < 64 && per_sm[dev] == 0) {
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm[dev], kern, P::THREADS, P::SMEM);
-        cudaDeviceGetAttribute(&num_sms[dev], cudaDevAttrMultiProcessorCount, dev);
-        if (per_sm[dev] < 1) per_sm[dev] = 1;
+    // resident blocks of the device, one word: a thread that finds it set must not find half of it
+    static std::atomic<int> resident[64];
+    int cap = dev >= 0 && dev < 64 ? resident[dev].load() : 148;
+    if (cap == 0) {
+        int per_sm = 0, num_sms = 0;
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, P::THREADS, P::SMEM);
+        cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev);
+        cap = (per_sm < 1 ? 1 : per_sm) * num_sms;
+        resident[dev] = cap;
     }
     const int64_t want = (M + P::TEAMS - 1) / P::TEAMS;
-    const int64_t cap = (int64_t)(dev >= 0 && dev < 64 ? per_sm[dev] * num_sms[dev] : 148);
     const int64_t blocks = want < cap ? want : cap;
     const float rk = (float)(1.0 / sqrt((double)P::K));
     kern<<<(unsigned)blocks, P::THREADS, P::SMEM, stream>>>(

@@ -483,7 +483,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(num_threads<BITS>(),
 // once per device and kernel instance.
 template <int BITS, int MODE>
 static int max_pairs(int num_sms) {
-    static int cache[64] = {};
+    static std::atomic<int> cache[64];
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 0 && dev < 64 && cache[dev] > 0) return cache[dev];
@@ -506,7 +506,7 @@ template <int BITS, int MODE>
 static cudaError_t launch_t(const GemmArgs &a, const CUtensorMap &mc, const CUtensorMap &mw,
                             void *out, int64_t tiles, int num_sms, cudaStream_t stream) {
     auto kern = ternary_gemm_pair_ts_kernel<BITS, MODE>;
-    static bool configured[64] = {};
+    static std::atomic<bool> configured[64];
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 0 && dev < 64 && !configured[dev]) {

@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
 template <int BITS, int MT, int MODE>
 static cudaError_t configure(int dev) {
-    static bool done[64] = {};
+    static std::atomic<bool> done[64];
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (done[dev]) return cudaSuccess;
     cudaError_t e = cudaFuncSetAttribute(ternary_gemm_skinny_kernel<BITS, MT, MODE>,
@@ -470,7 +470,7 @@ static cudaError_t configure(int dev) {
 // Clusters of S CTAs that can be resident at once on this device, for the largest instance
 // (MT = 64, which needs the most shared memory); looked up once per device and S.
 static int max_clusters(int S) {
-    static int cache[64][9] = {};
+    static std::atomic<int> cache[64][9];
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= 64 || S < 1 || S > 8) return 0;

@@ -520,7 +520,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
 // layout allows it), looked up once per device and kernel instance.
 template <int BITS, int MODE>
 static int max_pairs(int num_sms) {
-    static int cache[64] = {};
+    static std::atomic<int> cache[64];
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 0 && dev < 64 && cache[dev] > 0) return cache[dev];
@@ -544,7 +544,7 @@ static cudaError_t launch_tc_t(const GemmArgs &a, const CUtensorMap &mc, const C
                                const CUtensorMap &my, void *out, int64_t tiles, int num_sms,
                                cudaStream_t stream) {
     auto kern = ternary_gemm_tc_kernel<BITS, MODE>;
-    static bool configured[64] = {};
+    static std::atomic<bool> configured[64];
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 0 && dev < 64 && !configured[dev]) {

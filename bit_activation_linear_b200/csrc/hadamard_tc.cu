@@ -441,7 +441,7 @@ static cudaError_t launch_t(const CUtensorMap &map, int64_t M, void *codes, floa
                            int32_t *rowsum, float *zout, int *status, int num_sms,
                            cudaStream_t stream) {
     auto kern = hadamard_tc_kernel<LOGN, BITS, ABSMEAN, ZOUT>;
-    static bool configured[64] = {};
+    static std::atomic<bool> configured[64];
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 0 && dev < 64 && !configured[dev]) {

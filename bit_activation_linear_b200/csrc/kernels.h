@@ -2,6 +2,7 @@
 // Every launcher enqueues on `stream` and returns the cudaError_t of its launch.
 #pragma once
 
+#include <atomic>  // the launchers' per-device set-up: calls may come from several host threads
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

@@ -49,8 +49,6 @@
 // 67 us, 8 rows 69 us, 16 rows 95 us, 32 rows 174 us (the tensor-core kernel: 231 .. 240 us, so it
 // takes over above 32); one sequence of 131072 tokens, 4 rows, 57 us.  The stream runs at 5.7 TB/s
 // behind about 12 us of launch, dependent loads (lengths, page, codes), last chunks and join.
-#include <atomic>
-
 #include "kv_common.cuh"
 
 namespace bitnet {
@@ -635,7 +633,7 @@ cudaError_t launch_decode(const KvArgs &a, const AttentionArgs &at, void *ws, cu
         parts.joins = reinterpret_cast<int4 *>(parts.stats + rows * 2);
     }
     auto kern = kv_attention_kernel<D, NT>;
-    static std::atomic<bool> configured[64];  // calls may come from several host threads
+    static std::atomic<bool> configured[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;

@@ -26,7 +26,6 @@
 //
 // Every wait is bounded; after a time-out (recorded) each role leaves its loop and all meet at the
 // end, where tensor memory is freed.
-#include <atomic>
 #include <type_traits>
 
 #include "kv_common.cuh"
@@ -654,7 +653,7 @@ cudaError_t launch_tc(const KvArgs &a, const AttentionArgs &at, void *ws, cudaSt
         parts.stats = parts.sums + (size_t)blocks * kRows * D;
     }
     auto kern = kv_attention_tc_kernel<D>;
-    static std::atomic<bool> configured[64];  // calls may come from several host threads
+    static std::atomic<bool> configured[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;

@@ -132,3 +132,38 @@ def test_chains_of_layers_that_feed_one_another(B, M):
 
     check_chain(inputs(M, K), call, y)
     B.bitnet_sync_status()
+
+
+def test_forwards_from_several_host_threads(B):
+    """The first calls of several quantisers and products from eight threads at once, a stream each,
+    give what they give one after the other."""
+    import threading
+
+    jobs = []
+    for K in (128, 512, 1024, 4096, 16384):
+        W = synth.to_torch_bf16(synth.latent_weights(256, K, seed=K)).cuda()
+        jobs += [(K, M, bits, *B.bitnet_quantize_pack_weights(W)) for M in (1, 20, 100)
+                 for bits in (8, 4)]
+
+    def work(stream, out):
+        with torch.cuda.stream(stream):
+            for K, M, bits, Wp, gamma in jobs:
+                x = torch.randn((M, K), generator=torch.Generator(device="cuda").manual_seed(K),
+                                device="cuda").bfloat16()
+                out.append(B.bitnet_norm_bitlinear_forward(x, None, 1e-5, True, Wp, gamma, bits))
+                out.append(B.bitnet_hbitlinear_forward(x, Wp, gamma, bits))
+                out.append(B.bitnet_bitlinear_forward(x, Wp, gamma, bits))
+            stream.synchronize()
+
+    torch.cuda.synchronize()
+    outs = [[] for _ in range(8)]
+    threads = [threading.Thread(target=work, args=(torch.cuda.Stream(), out)) for out in outs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    want = []
+    work(torch.cuda.current_stream(), want)
+    for out in outs:
+        assert len(out) == len(want) and all(torch.equal(x, y) for x, y in zip(out, want))
+    B.bitnet_sync_status()
