@@ -954,7 +954,8 @@ def bitnet_kv_attention(cache: KvCache, Q: torch.Tensor, q_heads: int, q_start, 
                         causal: bool = True, Y=None, lse=None, want_lse: bool = False, ws=None,
                         stream=None):
     """Attention of new tokens Q (bf16 [tokens, q_heads * head_dim], rows may lie apart) over the
-    cached states of their sequences.  max_new: the most new tokens of any sequence.  scale
+    cached states of their sequences.  max_new: the most new tokens of any sequence; it chooses the
+    kernel for the whole batch, so prompts and single tokens belong in calls of their own.  scale
     defaults to 1 / sqrt(head_dim).  Returns (Y bf16 [tokens, q_heads * head_dim], lse float
     [tokens, q_heads] or None)."""
     L = _lib or load_library()

@@ -461,7 +461,7 @@ typedef struct {
  *   kv_len      [batch], each sequence's length with its new tokens (0 .. max_pages * page_tokens)
  *   page_table  [batch][max_pages]; the token at position p lies in page
  *               page_table[s][p / page_tokens].  Entries behind the length are not read.
- *   tokens      rows of the token matrices.
+ *   tokens      rows of the token matrices, up to 2^28; batch up to 2^20.
  * What the host cannot see is checked on the device: a sequence whose rows leave 0 .. tokens or
  * whose length leaves its page table, and a page number outside 0 .. num_pages - 1, make the next
  * bitnet_sync_status() return BITNET_ERR_INVALID.  Such a sequence is left out (its outputs stay
@@ -516,10 +516,17 @@ int bitnet_kv_cache_read(const bitnet_kv_cache *cache, const bitnet_kv_batch *ba
  * codes, or to 2^-31 of the row's largest one; sums are fp32.  Results do not depend on timing.
  * Q_dev, Y_dev  bf16 rows of q_heads * head_dim, ldq / ldy elements apart (multiples of 8); they
  *               must not overlap.
- * q_heads       kv_heads times 1 .. 128.
+ * q_heads       kv_heads times 1 .. 128; (tokens * q_heads / kv_heads / 256 + batch) * kv_heads up to
+ *               2^25 (else BITNET_ERR_UNSUPPORTED).
  * max_new       no sequence has more new tokens than this (>= 1): it chooses the kernel (up to 32
  *               rows, new tokens times query heads of a key head, stream the cache; more run on
  *               the tensor cores in tiles of 128 rows).  A sequence that has more is invalid.
+ *               One choice for the whole batch: a single token beside a prompt waits for a kernel
+ *               that is made for many rows, so prompts and decoding sequences belong in calls of
+ *               their own (8 key heads of 128, 4 query heads each: 2048 new tokens over 4096 and one
+ *               over 131072 take 2190 us in one call, 214 us in two; beside 16 single tokens over
+ *               8000, 286 and 213 us).  q_start + s, kv_len + s and page_table + s * max_pages give
+ *               the part of a batch from sequence s on.
  * scale         finite and > 0, usually 1 / sqrt(head_dim).
  * lse_dev       out: float [tokens][q_heads], or NULL.
  * ws_dev        scratch of ws_bytes >= bitnet_kv_attention_workspace_bytes(...) (0 for arguments
