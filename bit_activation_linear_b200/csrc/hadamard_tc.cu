@@ -180,14 +180,15 @@ __global__ void __launch_bounds__(Cfg<LOGN>::THREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bar->tmem_base;
-    // the product that reads these codes may start its own set-up now (it waits for this grid
-    // to complete before it reads anything)
-    pdl_launch_dependents();
 
     if (warp == 0) {
         // ------------------------------------------------------------------ TMA producer
         if (lane == 0) {
             pdl_wait();
+            // The product that reads these codes may start its own set-up now, and no earlier: it may
+            // load its weights before it waits for this grid, so whatever wrote them, the kernel in
+            // front of this one if that is the weights' quantiser, has to be complete by now.
+            pdl_launch_dependents();
             uint32_t issued = 0, ph = 0;
             for (int i = 0; i < my_tokens; ++i) {
                 const int s = i % C::X_SLOTS;

@@ -134,6 +134,35 @@ def test_chains_of_layers_that_feed_one_another(B, M):
     B.bitnet_sync_status()
 
 
+@pytest.mark.parametrize("hadamard", [False, True])
+@pytest.mark.parametrize("base3,M", [(False, 1), (False, 8), (False, 16), (False, 64), (False, 128),
+                                     (True, 1), (True, 8)])
+@pytest.mark.parametrize("K,N", [(256, 256), (8192, 2048), (16384, 512)])
+def test_chains_of_weights_and_forwards(B, M, hadamard, base3, K, N):
+    """Weights quantised into the same place right before each forward: the product may load them
+    before it waits for its own quantiser, not before they are there."""
+    ws = torch.empty(B.bitnet_workspace_bytes(M, K, N, 8), dtype=torch.uint8, device="cuda")
+    weights = [synth.to_torch_bf16(synth.latent_weights(N, K, seed=i)).cuda() for i in range(CALLS)]
+    pack = B.bitnet_quantize_pack_weights_base3 if base3 else B.bitnet_quantize_pack_weights
+    Wp, gamma = pack(weights[0])
+    Y = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+    wws = torch.empty(max(256, B.bitnet_weight_workspace_bytes(N, K)), dtype=torch.uint8,
+                      device="cuda")
+    x = inputs(M, K)[0]
+
+    def call(W):
+        pack(W, Wp, gamma, ws=wws)
+        if base3:
+            B.bitnet_bitlinear_forward_base3(x, Wp, gamma, hadamard, 0, Y=Y, ws=ws)
+        elif hadamard:
+            B.bitnet_hbitlinear_forward(x, Wp, gamma, 8, Y=Y, ws=ws)
+        else:
+            B.bitnet_bitlinear_forward(x, Wp, gamma, 8, Y=Y, ws=ws)
+
+    check_chain(weights, call, Y)
+    B.bitnet_sync_status()
+
+
 def test_forwards_from_several_host_threads(B):
     """The first calls of several quantisers and products from eight threads at once, a stream each,
     give what they give one after the other."""
