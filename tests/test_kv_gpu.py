@@ -1065,3 +1065,69 @@ def test_a_layer_step_residual_norm_qkv_cache_attention(B):
             want = np.concatenate(rows)
             assert np.all(np.abs(back[which].double().cpu().numpy() - want)
                           <= BF16_HALF * np.abs(want))
+
+
+@pytest.mark.parametrize("batch", [1, 4, 12])
+@pytest.mark.parametrize("bits", [8, 4])
+def test_a_replayed_decoding_step(B, batch, bits):
+    """Two layers of a decoder step captured once and replayed for 40 tokens, on one workspace and with
+    lengths that grow on the device, give what the same calls give one by one."""
+    width, q_heads, heads, dim, page = 512, 8, 2, 64, 16
+    n_qkv = (q_heads + 2 * heads) * dim
+    layers = []
+    for i in (1, 2):
+        layers.append([B.bitnet_quantize_pack_weights(
+            synth.to_torch_bf16(synth.latent_weights(n, k, seed=10 * i)).cuda())
+            for n, k in ((n_qkv, width), (width, q_heads * dim))])
+    table = torch.randperm(4 * batch, generator=torch.Generator().manual_seed(1)).int().cuda()
+    table = table.view(batch, 4)
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    first = torch.randn((batch, width), generator=gen, device="cuda").bfloat16()
+    start = torch.arange(batch + 1, dtype=torch.int32, device="cuda")
+    need = max(B.bitnet_workspace_bytes(batch, k, n, bits) for n, k in ((n_qkv, width),
+                                                                        (width, q_heads * dim)))
+
+    class State:
+        def __init__(self):
+            self.caches = [B.KvCache.empty(4 * batch, heads, dim, page, 16) for _ in layers]
+            for c in self.caches:
+                for t in (c.k_codes, c.v_codes, c.k_scales, c.v_scales):
+                    t.zero_()
+            self.length = torch.arange(batch, dtype=torch.int32, device="cuda")
+            self.stream, self.x = first.clone(), torch.zeros_like(first)
+            self.qkv = torch.empty((batch, n_qkv), dtype=torch.bfloat16, device="cuda")
+            self.y = torch.empty((batch, q_heads * dim), dtype=torch.bfloat16, device="cuda")
+            self.ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+
+        def step(self, wait=lambda: None):
+            self.length += 1
+            for cache, (qkv_w, out_w) in zip(self.caches, layers):
+                wait()
+                B.bitnet_residual_norm_bitlinear_forward(self.x, self.stream, None, 1e-5, *qkv_w, bits,
+                                                         H=self.stream, Y=self.qkv, ws=self.ws)
+                q, k, v = self.qkv.split([q_heads * dim, heads * dim, heads * dim], 1)
+                wait()
+                B.bitnet_kv_cache_append(cache, k, v, start, self.length, table)
+                wait()
+                B.bitnet_kv_attention(cache, q, q_heads, start, self.length, table, 1, Y=self.y)
+                wait()
+                B.bitnet_hbitlinear_forward(self.y, *out_w, bits, Y=self.x, ws=self.ws)
+                wait()
+
+    one, other = State(), State()
+    other.step()                       # first calls outside the capture
+    other = State()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        other.step()
+    for _ in range(40):
+        one.step(torch.cuda.synchronize)
+        graph.replay()
+    torch.cuda.synchronize()
+    B.bitnet_sync_status()
+    assert torch.isfinite(one.stream.float()).all()
+    for a, b in ((one.stream, other.stream), (one.x, other.x), (one.length, other.length)):
+        assert torch.equal(a, b)
+    for c, d in zip(one.caches, other.caches):
+        assert torch.equal(c.k_codes, d.k_codes) and torch.equal(c.v_codes, d.v_codes)
+        assert torch.equal(c.k_scales, d.k_scales) and torch.equal(c.v_scales, d.v_scales)
