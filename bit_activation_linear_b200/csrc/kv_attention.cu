@@ -46,8 +46,8 @@
 // both kinds of 16-byte reads are free of bank conflicts.
 //
 // Measured on B200 (D = 128, 32 ragged sequences of 2000 .. 8000 tokens, 8 key heads, 334 MB): 4 rows
-// 67 us, 8 rows 69 us, 16 rows 95 us, 32 rows 174 us (the tensor-core kernel: 231 .. 240 us, so it
-// takes over above 32); one sequence of 131072 tokens, 4 rows, 57 us.  The stream runs at 5.7 TB/s
+// 68 us, 8 rows 71 us, 16 rows 95 us, 32 rows 170 us (the tensor-core kernel: 240 us, so it takes
+// over above 32); one sequence of 131072 tokens, 4 rows, 57 us.  The stream runs at 5.7 TB/s
 // behind about 12 us of launch, dependent loads (lengths, page, codes), last chunks and join.
 #include "kv_common.cuh"
 

@@ -21,8 +21,8 @@
 // What bounds it: a step of 128 tokens takes about 5000 cycles, the MMAs in it 2048 and the
 // exponentials 2160 (16 a clock and SM): the chain scores -> softmax -> weights -> MMA of a tile is
 // latency-bound with one warp of each tile on a scheduler; the tiles run half a step apart so
-// that one's MMAs lie under the other's softmax.  6001 tokens over 7001 with 16 heads of 128: 279 us,
-// 705 TFLOP/s; 8192 tokens, 32 heads: 796 TFLOP/s; heads of 64: 447 TFLOP/s.
+// that one's MMAs lie under the other's softmax.  6001 tokens over 7001 with 16 heads of 128: 277 us,
+// 710 TFLOP/s; 8192 tokens, 32 heads: 798 TFLOP/s; heads of 64: 444 TFLOP/s.
 //
 // Every wait is bounded; after a time-out (recorded) each role leaves its loop and all meet at the
 // end, where tensor memory is freed.

@@ -13,9 +13,10 @@
 //
 // Bound by HBM: 6 bytes and the code an element, read once.  A row stays in the registers of its
 // threads between the addition and the codes (4 chunks of 8 values each, so K / 32 threads a row).
-// Measured on B200: 16383 x 4096 in 72 .. 76 us (6.2 .. 6.5 TB/s), 4096 x 2048 in 12 .. 14 us, one row
-// in the 3.4 us of a launch.  Rows above K = 32768 need more threads than a block has and are read
-// back: 4.2 TB/s at 33024 against 4.4 TB/s at 32768.
+// Measured on B200: 16383 x 4096 in 72 .. 76 us (5.9 .. 6.5 TB/s), 4096 x 2048 in 13 .. 14 us, one row in
+// the 3.4 us of a launch.  INT4 takes 83 us for the first: its mean is summed in double, as every
+// absmean of this library, and the conversions (two a value) bound it.  Rows above K = 32768 need more
+// threads than a block has and are read back: 4.5 TB/s at 33024 against 4.9 TB/s at 32768.
 #include "common.cuh"
 #include "kernels.h"
 
