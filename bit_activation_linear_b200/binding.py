@@ -885,11 +885,12 @@ def _rows(t, name: str, width: int, tokens, dev: int):
     shape, stride = t.shape, t.stride()
     if len(shape) == 2:
         cols = shape[1]
-        if cols > 1 and stride[1] != 1:
+        if cols > 1 and stride[1] != 1 and shape[0]:
             raise ValueError(f"the columns of {name} must be contiguous")
     elif len(shape) == 3:
         cols = shape[1] * shape[2]
-        if not t.is_contiguous() and (stride[2] != 1 or shape[1] > 1 and stride[1] != shape[2]):
+        if not t.is_contiguous() and shape[0] and (
+                stride[2] != 1 or shape[1] > 1 and stride[1] != shape[2]):
             raise ValueError(f"the heads of a row of {name} must lie one after the other")
     else:
         raise ValueError(f"{name} must have 2 or 3 dimensions")
@@ -897,7 +898,7 @@ def _rows(t, name: str, width: int, tokens, dev: int):
         raise ValueError(f"{name} has rows of {cols}, {width} wanted")
     if tokens is not None and shape[0] != tokens:
         raise ValueError(f"{name} has {shape[0]} rows, {tokens} wanted")
-    # a single row has no distance to the next one
+    # a single row has no distance to the next one, and no rows have no strides at all
     return t.data_ptr(), stride[0] if shape[0] > 1 else width
 
 

@@ -3,6 +3,7 @@ call here is answered by the host checks."""
 import ctypes
 import os
 
+import numpy as np
 import pytest
 import torch
 
@@ -182,3 +183,12 @@ def test_rows_of_one_head_in_any_layout(B):
         B._rows(heads[:, ::2], "K", 128, 6, -1)
     with pytest.raises(ValueError, match="one after the other"):
         B._rows(heads[:, :, ::2], "K", 128, 6, -1)
+
+
+def test_no_rows_in_any_layout(B):
+    """A matrix of no tokens has no distances (numpy's empty arrays come with other strides)."""
+    for t, width in ((torch.from_numpy(np.zeros((0, 64), np.float32)).bfloat16(), 64),
+                     (torch.empty((64, 0), dtype=torch.bfloat16).t(), 64),
+                     (torch.empty((64, 2, 0), dtype=torch.bfloat16).permute(2, 1, 0), 128)):
+        assert t.shape[0] == 0 and t.stride()[-1] != 1
+        assert B._rows(t, "Q", width, 0, -1)[1] == width
